@@ -418,6 +418,146 @@ int moe_set_gemm2_path(int32_t path);
  * on the reference pages. */
 int moe_test_set_stall(uint64_t stall_ns);
 
+/* ---------------------------------------------------------------- training
+ * The layer's training form, on rows in their own type instead of MX codes:
+ * layer norm in front of the router, tokens into expert order (moe_permute),
+ * the caller's products per expert over expert_offsets, the weighted sum back
+ * into tokens (moe_unpermute), the gradients of all of these and of the
+ * routing, and an AdamW step over the parameters, whose fp32 matrices
+ * moe_quantize_mxfp4 then takes.  The reference pages have forward passes
+ * only; "[SGLang] CUTLASS MoE", sections 1, 2 and 5 have the maps, the
+ * shuffle and the weighted sum that these follow.
+ *
+ * Types: every pointer to rows is of the shape's dtype; statistics, routing
+ * weights, their gradients and the parameters' gradients are fp32, and sums
+ * are taken in fp32.  Tensors are contiguous and aligned to their element.
+ * Rows move in 16-byte accesses where the row size and every row pointer are
+ * multiples of 16 bytes, else element by element, with the same results.
+ * Every result is bit-reproducible (no atomics).  Outputs do not alias inputs
+ * but where it is said.  A call with no tokens or rows launches nothing,
+ * except that sums over rows are written as zero. */
+enum { MOE_DTYPE_BF16 = 0, MOE_DTYPE_F16 = 1, MOE_DTYPE_F32 = 2 };
+
+/* rows [0, 2^31), cols [1, 2^20]; dtype of the rows, w_dtype of weight and
+ * bias (MOE_DTYPE_F32 or the rows'); eps >= 0 and finite. */
+typedef struct moe_norm_shape {
+    int64_t rows;
+    int32_t cols, dtype, w_dtype;
+    float eps;
+} moe_norm_shape;
+
+/* h = x + residual (rounded to dtype), mean and rstd = 1 / sqrt(var + eps) of
+ * each row of h, y = (h - mean) * rstd * weight + bias.  residual, weight and
+ * bias may be NULL (0, 1, 0); without a residual h is x and is not written.
+ * h may be x or residual itself. */
+int moe_layer_norm(const moe_norm_shape* shape, const void* x, const void* residual, const void* weight,
+                   const void* bias, void* h, void* y, float* mean, float* rstd, moe_stream_t stream);
+
+/* Bytes of moe_layer_norm_backward's workspace (partial sums over rows). */
+int moe_layer_norm_workspace_bytes(int64_t rows, int32_t cols, size_t* bytes);
+
+/* With xh = (h - mean) * rstd and a = dy * weight:
+ *   dx = rstd * (a - mean(a) - xh * mean(a * xh)) + dh
+ *   dweight = sum over rows of dy * xh,  dbias = sum over rows of dy
+ * dx is the gradient of x and of residual.  weight (1) and dh (0: the gradient
+ * that reaches h beside the norm) may be NULL; so may dweight and dbias, and
+ * without both the workspace (256-byte aligned) is not used.  dx may be dy or
+ * dh itself. */
+int moe_layer_norm_backward(const moe_norm_shape* shape, const void* dy, const void* h, const float* mean,
+                            const float* rstd, const void* weight, const void* dh, void* dx, float* dweight,
+                            float* dbias, void* workspace, size_t workspace_bytes, moe_stream_t stream);
+
+/* As the moe_shape fields of the same names, with any hidden in [1, 2^20]:
+ * 1 <= top_k <= 32, top_k <= E_global <= 1024, 1 <= E_local + num_shared <=
+ * 1024, num_shared in {0, 1}, 0 <= expert_offset, expert_offset + E_local <=
+ * E_global, T * (top_k + num_shared) < 2^24. */
+typedef struct moe_token_shape {
+    int32_t T, E_global, E_local, expert_offset, top_k, num_shared, hidden, dtype;
+} moe_token_shape;
+
+/* The maps of moe_sort in the caller's own buffers: topk_ids int32 [T, k'] ->
+ * expert_offsets int32 [E_local + num_shared + 1] (the first row of each
+ * expert, then the number of rows R), c_map int32 [T * k'] (slot -> row, -1
+ * for an expert that is not here) and a_map int32 [T * k'] (row -> slot;
+ * entries R and above are left as they are).  The workspace (256-byte
+ * aligned) holds the sort's tables during the call. */
+int moe_token_map_workspace_bytes(const moe_token_shape* shape, size_t* bytes);
+int moe_token_map(const moe_token_shape* shape, const int32_t* topk_ids, int32_t* a_map, int32_t* c_map,
+                  int32_t* expert_offsets, void* workspace, size_t workspace_bytes, moe_stream_t stream);
+
+/* rows[c_map[t, j]] = x[t]: x [T, H] -> rows [R, H] (rows from R on are not
+ * touched).  Every c_map entry is -1 or a row of its own in `rows`. */
+int moe_permute(const moe_token_shape* shape, const void* x, const int32_t* c_map, void* rows, moe_stream_t stream);
+
+/* dx[t] = sum over j with c_map[t, j] >= 0 of drows[c_map[t, j]], j ascending. */
+int moe_permute_backward(const moe_token_shape* shape, const void* drows, const int32_t* c_map, void* dx,
+                         moe_stream_t stream);
+
+/* out[t] = sum over j with c_map[t, j] >= 0 of topk_w[t, j] * rows[c_map[t,
+ * j]], j ascending; zero for a token with no row. */
+int moe_unpermute(const moe_token_shape* shape, const void* rows, const float* topk_w, const int32_t* c_map, void* out,
+                  moe_stream_t stream);
+
+/* drows[c_map[t, j]] = topk_w[t, j] * dout[t] and dtopk_w[t, j] = <dout[t],
+ * rows[c_map[t, j]]>, 0 where c_map is -1.  drows may be rows itself. */
+int moe_unpermute_backward(const moe_token_shape* shape, const void* dout, const void* rows, const float* topk_w,
+                           const int32_t* c_map, void* drows, float* dtopk_w, moe_stream_t stream);
+
+/* Gradient of moe_route: from its ids and weights and the weights' gradient
+ * fp32 [T, k'] to dlogits fp32 [T, E_global], w_j * (dw_j - sum_i w_i dw_i)
+ * over the picks and 0 elsewhere, and, with a shared expert, dshared_logit
+ * fp32 [T] = dw_s * shared_scale * a * (1 - a), a = sigmoid(shared_logit).
+ * A token's picks are distinct, as moe_route's are.  Of the shape it takes T,
+ * E_global, top_k and num_shared (every rank of an expert-parallel group has
+ * the whole row). */
+int moe_route_backward(const moe_token_shape* shape, const uint16_t* shared_logit, float shared_scale,
+                       const int32_t* topk_ids, const float* topk_w, const float* dtopk_w, float* dlogits,
+                       float* dshared_logit, moe_stream_t stream);
+
+/* AdamW states: MOE_STATE_F32 m and v in fp32; MOE_STATE_MXFP8 m and sqrt(v)
+ * as E4M3 codes with one E8M0 scale per 32 elements (zero bytes are the zero
+ * state). */
+enum { MOE_STATE_F32 = 0, MOE_STATE_MXFP8 = 1 };
+
+/* One parameter tensor (device pointers): p fp32 [n]; g [n] of the config's
+ * g_dtype; m, v [n], fp32 or uint8; m_scale, v_scale uint8 [ceil(n / 32)]
+ * (MXFP8 only). */
+typedef struct moe_adamw_tensor {
+    float* p;
+    const void* g;
+    void *m, *v;
+    uint8_t *m_scale, *v_scale;
+    int64_t n;
+} moe_adamw_tensor;
+
+/* step counts from 1; 0 <= beta < 1; eps >= 0; g_dtype MOE_DTYPE_BF16 or
+ * MOE_DTYPE_F32; seed: of the MXFP8 states' rounding, another one each step. */
+typedef struct moe_adamw_config {
+    double lr, beta1, beta2, eps, weight_decay;
+    int64_t step;
+    uint64_t seed;
+    int32_t g_dtype, state;
+} moe_adamw_config;
+
+/* One AdamW step over `count` tensors (a host array; read during the call),
+ * in place:
+ *   g' = g * grad_scale[0]  (device fp32, or NULL for 1; a value that is not
+ *        finite skips the step on the device: nothing changes)
+ *   m += (1 - beta1) * (g' - m),  v += (1 - beta2) * (g'^2 - v)
+ *   p = p * (1 - lr * weight_decay)
+ *       - lr / (1 - beta1^step) * m / (sqrt(v) / sqrt(1 - beta2^step) + eps)
+ * The update uses m and v before they are stored.  MXFP8 states: per block of
+ * 32 the scale 2^e, e = floor(log2 max|.|) - 7 within [-126, 126]; codes are
+ * rounded to one of the two neighbours with the probability of the distance,
+ * by 16 random bits of the SplitMix64 sequence that starts at seed (64-bit
+ * number c / 2 + 1 for elements c and c + 1 of even c, low half first; m takes
+ * the low 16 bits of a half, sqrt(v) the high), where c counts elements over
+ * the call's tensors, each tensor starting at a multiple of 32.  A sqrt(v) that
+ * is not zero keeps at least the smallest code.  Infinities are stored as NaN.
+ * A captured graph keeps the config of its capture. */
+int moe_adamw(const moe_adamw_tensor* tensors, int32_t count, const moe_adamw_config* config, const float* grad_scale,
+              moe_stream_t stream);
+
 /* Number of SMs the launches are sized for on the current device. */
 int moe_num_sms(int32_t* num_sms);
 

@@ -15,6 +15,8 @@ import os
 import torch
 
 from . import build as _build
+from . import train as _train
+from .train import *  # noqa: F401,F403 -- the training form's calls, under the same names
 
 __all__ = [
     "MoeShape", "MoeWeights", "MoeError", "lib", "moe_is_supported", "moe_workspace_bytes",
@@ -25,7 +27,7 @@ __all__ = [
     "MoeNvfp4", "moe_quantize_nvfp4", "moe_pack_weights_nvfp4", "moe_layer_nvfp4", "moe_layer_nvfp4_events",
     "quantize_expert_weights_nvfp4",
     "workspace", "MOE_OK", "MOE_ERR_TIMEOUT", "MOE_ERR_WORKSPACE",
-]
+] + _train.__all__
 
 MOE_OK = 0
 GEMM2_AUTO, GEMM2_SPLIT, GEMM2_DENSE = 0, 1, 2  # moe_set_gemm2_path
@@ -152,6 +154,7 @@ _SIGS = {
     "moe_layer_nvfp4_events": [ctypes.c_void_p] * 9 + [ctypes.c_size_t] + [ctypes.c_void_p] * 3,
     "moe_num_sms": [ctypes.c_void_p],
     "moe_layer_launch_count": [ctypes.c_void_p, ctypes.c_void_p],
+    **_train.SIGS,
 }
 
 

@@ -1,0 +1,66 @@
+// Gradient of the routing (top-k, softmax over the picks, the shared expert's
+// sigmoid) with respect to the logits.  The picks themselves have none, so
+//   dlogits[t, id_j] = w_j (dw_j - sum_i w_i dw_i)   for the picks, 0 elsewhere
+//   dshared[t] = dw_s scale a (1 - a),  a = sigmoid(logit)
+// A warp takes a token: lane j holds pick j, the row is put together in
+// shared memory and written whole.  The row's write is nearly all the
+// traffic.
+#include "train.cuh"
+
+namespace moe {
+
+namespace {
+
+constexpr int kRgWarps = 8;
+
+__global__ void __launch_bounds__(kRgWarps * 32) route_grad_kernel(RouteGradParams p, int vec) {
+    extern __shared__ float4 s_rows[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int pad = (p.Eg + 3) & ~3;
+    float* row = reinterpret_cast<float*>(s_rows) + warp * pad;
+    for (int e = lane; e < pad; e += 32) row[e] = 0.f;
+    __syncwarp();
+    for (int64_t t = static_cast<int64_t>(blockIdx.x) * kRgWarps + warp; t < p.T;
+         t += static_cast<int64_t>(gridDim.x) * kRgWarps) {
+        const int64_t s0 = t * p.kp;
+        int id = -1;
+        float w = 0.f, d = 0.f;
+        if (lane < p.k) {
+            id = p.ids[s0 + lane];
+            w = p.w[s0 + lane];
+            d = p.dw[s0 + lane];
+        }
+        float sum = w * d;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        const bool pick = lane < p.k && id >= 0 && id < p.Eg;
+        if (pick) row[id] = w * (d - sum);
+        if (p.S && lane == 0) {
+            const float a = 1.f / (1.f + expf(-bf16_bits_to_float(p.shared_logit[t])));
+            p.dshared[t] = p.dw[s0 + p.k] * p.shared_scale * a * (1.f - a);
+        }
+        __syncwarp();
+        float* out = p.dlogits + t * p.Eg;
+        if (vec) {
+            for (int c = lane; c < p.Eg / 4; c += 32)
+                reinterpret_cast<float4*>(out)[c] = reinterpret_cast<const float4*>(row)[c];
+        } else {
+            for (int e = lane; e < p.Eg; e += 32) out[e] = row[e];
+        }
+        __syncwarp();
+        if (pick) row[id] = 0.f;
+        __syncwarp();
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_route_grad(const RouteGradParams& p, cudaStream_t st) {
+    const size_t smem = size_t(kRgWarps) * ((p.Eg + 3) & ~3) * sizeof(float);  // at most 32 KB
+    const int64_t ctas = (p.T + kRgWarps - 1) / kRgWarps;
+    const bool vec = p.Eg % 4 == 0 && (reinterpret_cast<uintptr_t>(p.dlogits) & 15) == 0;
+    return launch_kernel(route_grad_kernel, dim3(static_cast<unsigned>(ctas < 152 * 6 ? ctas : 152 * 6)),
+                         dim3(kRgWarps * 32), smem, st, false, p, vec ? 1 : 0);
+}
+
+}  // namespace moe

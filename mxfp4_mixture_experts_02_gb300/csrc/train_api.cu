@@ -1,0 +1,312 @@
+// C entries of the training operators around the experts (declared in
+// include/moe_api.h): argument checks on the host, then the launches.
+#include <cmath>
+#include <memory>
+#include <new>
+
+#include "train.cuh"
+
+namespace moe {
+namespace {
+
+bool on(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+int rc_of(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
+cudaStream_t cu(moe_stream_t s) { return reinterpret_cast<cudaStream_t>(s); }
+
+// Bytes per element, 0 for a type the operators do not take.
+int elem_bytes(int dtype) {
+    return dtype == MOE_DTYPE_F32 ? 4 : (dtype == MOE_DTYPE_BF16 || dtype == MOE_DTYPE_F16) ? 2 : 0;
+}
+
+// Null pointers (absent operands) are on every boundary.
+template <typename... P>
+bool all_on(uintptr_t a, P... p) {
+    return (on(p, a) && ...);
+}
+
+// Rows move in 16-byte accesses when every row starts on such a boundary.
+bool wide_rows(int64_t cols, int bytes) { return cols * bytes % 16 == 0; }
+
+int check_norm(const moe_norm_shape* s) {
+    if (!s) return MOE_ERR_NULL;
+    const int b = elem_bytes(s->dtype);
+    if (!b || (s->w_dtype != MOE_DTYPE_F32 && s->w_dtype != s->dtype)) return MOE_ERR_SHAPE;
+    if (s->rows < 0 || s->rows > 0x7FFFFFFF || s->cols < 1 || s->cols > (1 << 20)) return MOE_ERR_SHAPE;
+    if (!(s->eps >= 0.f) || !(s->eps <= 3.0e38f)) return MOE_ERR_SHAPE;
+    return MOE_OK;
+}
+
+size_t norm_ws_bytes(int64_t rows, int32_t cols) {
+    const int64_t parts = rows < kNormMaxPartials ? (rows > 0 ? rows : 1) : kNormMaxPartials;
+    return static_cast<size_t>(parts) * 2 * cols * sizeof(float);
+}
+
+int check_slots(const moe_token_shape* s) {
+    if (!s) return MOE_ERR_NULL;
+    if (s->top_k < 1 || s->top_k > 32 || s->top_k > s->E_global || s->E_global > 1024) return MOE_ERR_SHAPE;
+    if (s->num_shared < 0 || s->num_shared > 1) return MOE_ERR_SHAPE;
+    if (s->T < 0 || static_cast<int64_t>(s->T) * (s->top_k + s->num_shared) >= (1 << 24)) return MOE_ERR_SHAPE;
+    return MOE_OK;
+}
+
+int check_tokens(const moe_token_shape* s) {
+    const int rc = check_slots(s);
+    if (rc) return rc;
+    if (!elem_bytes(s->dtype) || s->hidden < 1 || s->hidden > (1 << 20)) return MOE_ERR_SHAPE;
+    if (s->E_local < 1 || s->E_local + s->num_shared > 1024) return MOE_ERR_SHAPE;
+    if (s->expert_offset < 0 || s->expert_offset > s->E_global - s->E_local) return MOE_ERR_SHAPE;
+    return MOE_OK;
+}
+
+// The sort's own tables, beside the caller's maps: header, counts, virtual
+// experts of 128 rows and the large sort's histograms.
+struct MapLayout {
+    size_t header, counts, vinfo, groups, vbase, hist, total;
+};
+
+MapLayout map_layout(const moe_token_shape& s) {
+    const size_t n = static_cast<size_t>(s.T) * (s.top_k + s.num_shared), Et = s.E_local + s.num_shared;
+    const size_t V = Et + n / 128;
+    MapLayout L{};
+    size_t o = 0;
+    auto take = [&](size_t bytes) {
+        const size_t at = o;
+        o = align256(o + bytes);
+        return at;
+    };
+    L.header = take(kHeaderWords * 4);
+    L.counts = take(Et * 4);
+    L.vinfo = take(V * 16);
+    L.groups = take(V * 16);
+    L.vbase = take(Et * 4);
+    L.hist = take((n + 4095) / 4096 * Et * 4);
+    L.total = o;
+    return L;
+}
+
+TokenParams token_params(const moe_token_shape& s, const void* src, const int32_t* c_map, const float* w, void* dst) {
+    TokenParams p{};
+    p.src = src;
+    p.w = w;
+    p.c_map = c_map;
+    p.dst = dst;
+    p.T = s.T;
+    p.kp = s.top_k + s.num_shared;
+    p.H = s.hidden;
+    return p;
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+int moe_layer_norm_workspace_bytes(int64_t rows, int32_t cols, size_t* bytes) {
+    if (!bytes) return MOE_ERR_NULL;
+    if (rows < 0 || cols < 1 || cols > (1 << 20)) return MOE_ERR_SHAPE;
+    *bytes = norm_ws_bytes(rows, cols);
+    return MOE_OK;
+}
+
+int moe_layer_norm(const moe_norm_shape* s, const void* x, const void* residual, const void* weight, const void* bias,
+                   void* h, void* y, float* mean, float* rstd, moe_stream_t stream) {
+    int rc = check_norm(s);
+    if (rc) return rc;
+    if (s->rows == 0) return MOE_OK;
+    if (!x || !y || !mean || !rstd || (residual && !h)) return MOE_ERR_NULL;
+    const int b = elem_bytes(s->dtype), wb = elem_bytes(s->w_dtype);
+    if (!all_on(b, x, residual, h, y) || !all_on(wb, weight, bias) || !all_on(4, mean, rstd)) return MOE_ERR_ALIGN;
+    NormParams p{x, residual, weight, bias, residual ? h : nullptr, y, mean, rstd, s->rows, s->cols,
+                 s->w_dtype == MOE_DTYPE_F32, s->eps};
+    const bool vec = wide_rows(s->cols, b) && all_on(16, x, residual, p.h, y, weight, bias);
+    return rc_of(launch_norm(p, s->dtype, vec, cu(stream)));
+}
+
+int moe_layer_norm_backward(const moe_norm_shape* s, const void* dy, const void* h, const float* mean,
+                            const float* rstd, const void* weight, const void* dh, void* dx, float* dweight,
+                            float* dbias, void* ws, size_t ws_bytes, moe_stream_t stream) {
+    int rc = check_norm(s);
+    if (rc) return rc;
+    if (s->rows > 0 && (!dy || !h || !mean || !rstd || !dx)) return MOE_ERR_NULL;
+    const bool sums = dweight || dbias;
+    if (sums && !ws) return MOE_ERR_NULL;
+    const int b = elem_bytes(s->dtype), wb = elem_bytes(s->w_dtype);
+    if (!all_on(b, dy, h, dh, dx) || !on(weight, wb) || !all_on(4, mean, rstd, dweight, dbias) ||
+        (sums && !on(ws, 256)))
+        return MOE_ERR_ALIGN;
+    if (sums && ws_bytes < norm_ws_bytes(s->rows, s->cols)) return MOE_ERR_WORKSPACE;
+    if (s->rows == 0 && !sums) return MOE_OK;
+    NormGradParams p{dy, h, weight, dh, mean, rstd, dx, dweight, dbias, sums ? static_cast<float*>(ws) : nullptr,
+                     s->rows, s->cols, s->w_dtype == MOE_DTYPE_F32};
+    const bool vec = wide_rows(s->cols, b) && all_on(16, dy, h, weight, dh, dx);
+    return rc_of(launch_norm_grad(p, s->dtype, vec, cu(stream)));
+}
+
+int moe_token_map_workspace_bytes(const moe_token_shape* s, size_t* bytes) {
+    int rc = check_tokens(s);
+    if (rc) return rc;
+    if (!bytes) return MOE_ERR_NULL;
+    *bytes = map_layout(*s).total;
+    return MOE_OK;
+}
+
+int moe_token_map(const moe_token_shape* s, const int32_t* ids, int32_t* a_map, int32_t* c_map,
+                  int32_t* expert_offsets, void* ws, size_t ws_bytes, moe_stream_t stream) {
+    int rc = check_tokens(s);
+    if (rc) return rc;
+    if (!expert_offsets || !ws || (s->T > 0 && (!ids || !a_map || !c_map))) return MOE_ERR_NULL;
+    if (!all_on(4, ids, a_map, c_map, expert_offsets) || !on(ws, 256)) return MOE_ERR_ALIGN;
+    const MapLayout L = map_layout(*s);
+    if (ws_bytes < L.total) return MOE_ERR_WORKSPACE;
+    auto in = [&](size_t off) { return static_cast<uint8_t*>(ws) + off; };
+    SortParams p{};
+    p.ids = ids;
+    p.header = reinterpret_cast<int32_t*>(in(L.header));
+    p.counts = reinterpret_cast<int32_t*>(in(L.counts));
+    p.offsets = expert_offsets;
+    p.vinfo = reinterpret_cast<int4*>(in(L.vinfo));
+    p.groups = reinterpret_cast<int4*>(in(L.groups));
+    p.a_map = a_map;
+    p.c_map = c_map;
+    p.vbase = reinterpret_cast<int32_t*>(in(L.vbase));
+    p.cta_hist = reinterpret_cast<int32_t*>(in(L.hist));
+    p.T = s->T;
+    p.kp = s->top_k + s->num_shared;
+    p.Eg = s->E_global;
+    p.E = s->E_local;
+    p.off = s->expert_offset;
+    p.S = s->num_shared;
+    p.Et = s->E_local + s->num_shared;
+    p.B = 128;
+    p.G = 1;
+    p.H = s->hidden;
+    p.gemm2_force = MOE_GEMM2_SPLIT;
+    return rc_of(launch_sort(p, cu(stream), false));
+}
+
+int moe_permute(const moe_token_shape* s, const void* x, const int32_t* c_map, void* rows, moe_stream_t stream) {
+    int rc = check_tokens(s);
+    if (rc) return rc;
+    if (s->T == 0) return MOE_OK;
+    if (!x || !c_map || !rows) return MOE_ERR_NULL;
+    const int b = elem_bytes(s->dtype);
+    if (!all_on(b, x, rows) || !on(c_map, 4)) return MOE_ERR_ALIGN;
+    const bool vec = wide_rows(s->hidden, b) && all_on(16, x, rows);
+    return rc_of(launch_permute(token_params(*s, x, c_map, nullptr, rows), s->dtype, vec, cu(stream), false));
+}
+
+int moe_permute_backward(const moe_token_shape* s, const void* drows, const int32_t* c_map, void* dx,
+                         moe_stream_t stream) {
+    int rc = check_tokens(s);
+    if (rc) return rc;
+    if (s->T == 0) return MOE_OK;
+    if (!drows || !c_map || !dx) return MOE_ERR_NULL;
+    const int b = elem_bytes(s->dtype);
+    if (!all_on(b, drows, dx) || !on(c_map, 4)) return MOE_ERR_ALIGN;
+    const bool vec = wide_rows(s->hidden, b) && all_on(16, drows, dx);
+    return rc_of(launch_unpermute(token_params(*s, drows, c_map, nullptr, dx), s->dtype, vec, cu(stream)));
+}
+
+int moe_unpermute(const moe_token_shape* s, const void* rows, const float* topk_w, const int32_t* c_map, void* out,
+                  moe_stream_t stream) {
+    int rc = check_tokens(s);
+    if (rc) return rc;
+    if (s->T == 0) return MOE_OK;
+    if (!rows || !topk_w || !c_map || !out) return MOE_ERR_NULL;
+    const int b = elem_bytes(s->dtype);
+    if (!all_on(b, rows, out) || !all_on(4, topk_w, c_map)) return MOE_ERR_ALIGN;
+    const bool vec = wide_rows(s->hidden, b) && all_on(16, rows, out);
+    return rc_of(launch_unpermute(token_params(*s, rows, c_map, topk_w, out), s->dtype, vec, cu(stream)));
+}
+
+int moe_unpermute_backward(const moe_token_shape* s, const void* dout, const void* rows, const float* topk_w,
+                           const int32_t* c_map, void* drows, float* dtopk_w, moe_stream_t stream) {
+    int rc = check_tokens(s);
+    if (rc) return rc;
+    if (s->T == 0) return MOE_OK;
+    if (!dout || !rows || !topk_w || !c_map || !drows || !dtopk_w) return MOE_ERR_NULL;
+    const int b = elem_bytes(s->dtype);
+    if (!all_on(b, dout, rows, drows) || !all_on(4, topk_w, c_map, dtopk_w)) return MOE_ERR_ALIGN;
+    const bool vec = wide_rows(s->hidden, b) && all_on(16, dout, rows, drows);
+    TokenParams p = token_params(*s, rows, c_map, topk_w, drows);
+    p.dout = dout;
+    p.dw = dtopk_w;
+    return rc_of(launch_unpermute_grad(p, s->dtype, vec, cu(stream)));
+}
+
+int moe_route_backward(const moe_token_shape* s, const uint16_t* shared_logit, float shared_scale, const int32_t* ids,
+                       const float* topk_w, const float* dtopk_w, float* dlogits, float* dshared_logit,
+                       moe_stream_t stream) {
+    int rc = check_slots(s);
+    if (rc) return rc;
+    if (s->T == 0) return MOE_OK;
+    if (!ids || !topk_w || !dtopk_w || !dlogits || (s->num_shared && (!shared_logit || !dshared_logit)))
+        return MOE_ERR_NULL;
+    if (!all_on(4, ids, topk_w, dtopk_w, dlogits, dshared_logit) || !on(shared_logit, 2)) return MOE_ERR_ALIGN;
+    RouteGradParams p{ids, topk_w, dtopk_w, shared_logit, dlogits, dshared_logit, s->T, s->E_global, s->top_k,
+                      s->num_shared, s->top_k + s->num_shared, shared_scale};
+    return rc_of(launch_route_grad(p, cu(stream)));
+}
+
+int moe_adamw(const moe_adamw_tensor* tensors, int32_t count, const moe_adamw_config* c, const float* grad_scale,
+              moe_stream_t stream) {
+    if (!c || (count > 0 && !tensors)) return MOE_ERR_NULL;
+    if (count < 0 || c->step < 1 || (c->g_dtype != MOE_DTYPE_BF16 && c->g_dtype != MOE_DTYPE_F32)) return MOE_ERR_SHAPE;
+    if (c->state != MOE_STATE_F32 && c->state != MOE_STATE_MXFP8) return MOE_ERR_SHAPE;
+    auto in01 = [](double v) { return v >= 0.0 && v < 1.0; };
+    auto finite = [](double v) { return v >= -3.0e38 && v <= 3.0e38; };
+    if (!in01(c->beta1) || !in01(c->beta2) || !finite(c->lr) || !finite(c->weight_decay) || !finite(c->eps) ||
+        c->eps < 0.0)
+        return MOE_ERR_SHAPE;
+    const bool mx = c->state == MOE_STATE_MXFP8;
+    const int gb = elem_bytes(c->g_dtype);
+    for (int32_t i = 0; i < count; ++i) {  // every check before the first launch
+        const moe_adamw_tensor& t = tensors[i];
+        if (t.n < 0 || t.n > (int64_t(1) << 40)) return MOE_ERR_SHAPE;
+        if (t.n == 0) continue;
+        if (!t.p || !t.g || !t.m || !t.v || (mx && (!t.m_scale || !t.v_scale))) return MOE_ERR_NULL;
+        if (!on(t.p, 4) || !on(t.g, gb) || (!mx && !all_on(4, t.m, t.v))) return MOE_ERR_ALIGN;
+    }
+    if (!on(grad_scale, 4)) return MOE_ERR_ALIGN;
+    // the parameters of a launch: 32 KB, so not on the stack of a caller's thread
+    std::unique_ptr<AdamwBatch<kAdamwMaxTensors>> b(new (std::nothrow) AdamwBatch<kAdamwMaxTensors>());
+    if (!b) return MOE_ERR_CUDA;
+    b->grad_scale = grad_scale;
+    b->seed = c->seed;
+    b->beta1 = static_cast<float>(c->beta1);
+    b->one_minus_beta1 = static_cast<float>(1.0 - c->beta1);
+    b->beta2 = static_cast<float>(c->beta2);
+    b->one_minus_beta2 = static_cast<float>(1.0 - c->beta2);
+    b->decay = static_cast<float>(1.0 - c->lr * c->weight_decay);
+    b->step_size = static_cast<float>(c->lr / (1.0 - std::pow(c->beta1, static_cast<double>(c->step))));
+    b->inv_root_bc2 = static_cast<float>(1.0 / std::sqrt(1.0 - std::pow(c->beta2, static_cast<double>(c->step))));
+    b->eps = static_cast<float>(c->eps);
+    int64_t counter = 0, items = 0;
+    auto flush = [&]() -> int {
+        if (!b->count) return MOE_OK;
+        b->items = static_cast<uint32_t>(items);
+        const int r = rc_of(launch_adamw(*b, c->g_dtype, mx, cu(stream)));
+        b->count = 0;
+        items = 0;
+        return r;
+    };
+    for (int32_t i = 0; i < count; ++i) {
+        const moe_adamw_tensor& t = tensors[i];
+        if (t.n == 0) continue;
+        const int64_t mine = (t.n + kAdamwItem - 1) / kAdamwItem;
+        if (b->count == kAdamwMaxTensors || items + mine > 0xFFFFFFFFll) {
+            const int rc = flush();
+            if (rc) return rc;
+        }
+        AdamwTensor& k = b->t[b->count++];
+        k = AdamwTensor{t.p, t.g, t.m, t.v, t.m_scale, t.v_scale, t.n, counter, static_cast<uint32_t>(items), 0};
+        k.vec = on(t.p, 16) && on(t.g, 16) && (mx ? all_on(8, t.m, t.v) : all_on(16, t.m, t.v));
+        counter += (t.n + 31) & ~int64_t(31);
+        items += mine;
+    }
+    return flush();
+}
+
+}  // extern "C"
