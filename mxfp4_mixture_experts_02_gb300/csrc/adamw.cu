@@ -57,9 +57,12 @@ template <typename G>
 __device__ __forceinline__ void load8(float (&g)[kE], const G* p) {
 #pragma unroll
     for (int i = 0; i < kE; i += kFull<G>) {
-        const Vec<G, kFull<G>> v = load_vec<G, kFull<G>>(p + i);
+        Vec<G, kFull<G>> v;
+        float f[kFull<G>];
+        v.load(p + i);
+        v.get(f);
 #pragma unroll
-        for (int u = 0; u < kFull<G>; ++u) g[i + u] = to_f32(v.v[u]);
+        for (int u = 0; u < kFull<G>; ++u) g[i + u] = f[u];
     }
 }
 
@@ -219,7 +222,7 @@ __global__ void __launch_bounds__(kAdamwThreads) adamw_kernel(const __grid_const
 }  // namespace
 
 cudaError_t launch_adamw(const AdamwBatch<kAdamwMaxTensors>& b, int g_dtype, bool mx, cudaStream_t st) {
-    const dim3 grid(b.items < 152u * 8 ? b.items : 152u * 8);
+    const dim3 grid(b.items < kSms * 8u ? b.items : kSms * 8u);
     auto go = [&](auto kernel) { return launch_kernel(kernel, grid, dim3(kAdamwThreads), 0, st, false, b); };
     if (g_dtype == MOE_DTYPE_F32) return mx ? go(adamw_kernel<float, true>) : go(adamw_kernel<float, false>);
     return mx ? go(adamw_kernel<__nv_bfloat16, true>) : go(adamw_kernel<__nv_bfloat16, false>);

@@ -3,16 +3,25 @@
 //   h = x + r (rounded to the rows' type: the stream is stored so)
 //   mean = sum h / n,  rstd = (sum (h - mean)^2 / n + eps)^-1/2
 //   y = (h - mean) rstd w + b
-// A row is read once and stays in registers, so the variance is the sum of
-// squared distances from the mean (no cancellation); sums are in 32 bits.
+// and its gradient.  Both passes are bound by the rows they read and write.
+// A CTA (or, for short rows, a group of a warp's lanes) walks over rows; a
+// thread owns the same columns of each, so weight, bias and the gradient's
+// column sums stay in its registers.  The rows after the present one are on
+// their way meanwhile: each thread copies its own columns into its own slots
+// of a ring in shared memory, which needs no barrier and no registers.
+//
+// Rows off the 16-byte grid: rows 8 apart start at the same place between grid
+// points, so a CTA takes rows 8 n apart, and its threads keep the same pieces
+// of the grid, which reach over the ends of the row.
+#include <algorithm>
+
 #include "train.cuh"
 
 namespace moe {
 
 namespace {
 
-// Sum over the L lanes of a sub-warp group (L a power of two, all lanes of
-// the warp take part).
+// Sum over the L lanes of a group (L a power of two, the whole warp takes part).
 __device__ __forceinline__ float lanes_sum(float v, int L) {
     for (int o = L >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
@@ -27,333 +36,606 @@ __device__ __forceinline__ float block_sum(float v, float* s_part) {
     return lanes_sum(lane < nw ? s_part[lane] : 0.f, 32);
 }
 
-constexpr int kWarpRowThreads = 128;
+// The rows on their way: S stages of N tensors, V accesses per thread and
+// tensor, slot (stage, tensor, access, thread), and a pair of statistics for
+// every warp or group; a stage is named by its byte offset.  Strides are those
+// of the largest CTA (C threads), so they are constants.  Single 16-bit
+// elements are below the smallest asynchronous copy and are loaded when their
+// turn comes.
+template <typename T, int LIE, int V, int S, int N, int C, bool GROUP>
+struct Ring {
+    static constexpr int VE = kVe<T, LIE>, kBytes = static_cast<int>(sizeof(T)) * VE;
+    static constexpr bool kAsync = kBytes >= 4;
+    static constexpr uint32_t kAccess = C * kBytes, kTensor = V * kAccess;
+    static constexpr uint32_t kStats = kAsync ? N * kTensor : 0, kStage = kStats + C / (GROUP ? 1 : 32) * 8,
+                              kEnd = S * kStage;
+    uint32_t mine, stats;  // this thread's first slot; the first pair
 
-// V accesses of VE elements per thread hold a row.  WARP: L <= 32 lanes take
-// a row, 128 / L rows per CTA; else the CTA takes one row and L = blockDim.x.
-template <typename T, int VE, int V, bool WARP>
-__global__ void __launch_bounds__(WARP ? kWarpRowThreads : 1024) norm_kernel(NormParams p, int L) {
-    __shared__ float s_part[2][32];
-    const int64_t row = WARP ? (static_cast<int64_t>(blockIdx.x) * kWarpRowThreads + threadIdx.x) / L : blockIdx.x;
-    const int lane = WARP ? threadIdx.x & (L - 1) : threadIdx.x;
-    const int nvec = p.cols / VE;
-    const bool live = row < p.rows;  // lanes past the last row take part in the shuffles
-    const int64_t base = row * p.cols;
-    const T* x = static_cast<const T*>(p.x) + base;
-    Vec<T, VE> h[V];
+    __device__ __forceinline__ explicit Ring(void* base)
+        : mine(ptx::smem_u32(base) + threadIdx.x * kBytes), stats(ptx::smem_u32(base) + kStats) {}
+    __device__ __forceinline__ static uint32_t next(uint32_t st) { return st == kEnd - kStage ? 0u : st + kStage; }
+    // An access that no row fills reads as zero.
+    __device__ __forceinline__ void clear(int t, int i) const {
+        if constexpr (kAsync)
+            for (int s = 0; s < S; ++s)
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-        if (live && i * L + lane < nvec) h[i] = load_vec<T, VE>(x + static_cast<int64_t>(i * L + lane) * VE);
-    if (p.residual) {
-        const T* r = static_cast<const T*>(p.residual) + base;
-        T* ho = static_cast<T*>(p.h) + base;
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-            if (live && i * L + lane < nvec) {
-                const int64_t c = static_cast<int64_t>(i * L + lane) * VE;
-                const Vec<T, VE> a = load_vec<T, VE>(r + c);
-#pragma unroll
-                for (int u = 0; u < VE; ++u) h[i].v[u] = from_f32<T>(to_f32(h[i].v[u]) + to_f32(a.v[u]));
-                store_vec<T, VE>(ho + c, h[i]);
-            }
+                for (int b = 0; b < kBytes; b += 4)
+                    ptx::st_shared_4(mine + s * kStage + t * kTensor + i * kAccess + b, 0u);
     }
-    float s = 0.f;
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-        if (live && i * L + lane < nvec) {
-#pragma unroll
-            for (int u = 0; u < VE; ++u) s += to_f32(h[i].v[u]);
-        }
-    const float inv_n = 1.0f / static_cast<float>(p.cols);
-    const float mean = (WARP ? lanes_sum(s, L) : block_sum(s, s_part[0])) * inv_n;
-    float q = 0.f;
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-        if (live && i * L + lane < nvec) {
-#pragma unroll
-            for (int u = 0; u < VE; ++u) {
-                const float d = to_f32(h[i].v[u]) - mean;
-                q += d * d;
-            }
-        }
-    const float var = (WARP ? lanes_sum(q, L) : block_sum(q, s_part[1])) * inv_n;
-    const float rstd = 1.0f / sqrtf(var + p.eps);
-    if (!live) return;
-    if (lane == 0) {
-        p.mean[row] = mean;
-        p.rstd[row] = rstd;
+    // The access from column c on, at src; columns past the row are not read
+    // (the tensor may end there) and become zero.
+    __device__ __forceinline__ void fetch(uint32_t st, int t, int i, const char* src, int c, int cols) const {
+        const uint32_t to = mine + st + t * kTensor + i * kAccess;
+        if constexpr (LIE == kOff)
+            ptx::cp_async_16_part(to, src, min((cols - c) * static_cast<int>(sizeof(T)), 16));
+        else if constexpr (kBytes == 16) ptx::cp_async_16(to, src);
+        else if constexpr (kAsync) ptx::cp_async_4(to, src);
     }
-    T* y = static_cast<T*>(p.y) + base;
+    // live: the row is there
+    __device__ __forceinline__ void take(float* to, uint32_t st, int t, int i, const char* src, int c, int cols,
+                                         bool live) const {
+        Vec<T, VE> v;
+        const uint32_t at = mine + st + t * kTensor + i * kAccess;
+        if constexpr (kBytes == 16) v.w = ptx::ld_shared_16(at);
+        else if constexpr (kAsync) v.v = __uint_as_float(ptx::ld_shared_4(at));
+        else v.v = live && c < cols ? *reinterpret_cast<const T*>(src) : from_f32<T>(0.f);
+        float f[VE];
+        v.get(f);
+        if (LIE == kOff && c < 0) {  // the end of the row before
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-        if (i * L + lane < nvec) {
-            const int64_t c = static_cast<int64_t>(i * L + lane) * VE;
-            float w[VE], b[VE];
-#pragma unroll
-            for (int u = 0; u < VE; ++u) w[u] = 1.f, b[u] = 0.f;
-            if (p.weight) load_param<T, VE>(w, p.weight, p.w_f32, c);
-            if (p.bias) load_param<T, VE>(b, p.bias, p.w_f32, c);
-            Vec<T, VE> o;
-#pragma unroll
-            for (int u = 0; u < VE; ++u) o.v[u] = from_f32<T>((to_f32(h[i].v[u]) - mean) * rstd * w[u] + b[u]);
-            store_vec<T, VE>(y + c, o);
+            for (int u = 0; u < VE; ++u)
+                if (c + u < 0) f[u] = 0.f;
         }
+#pragma unroll
+        for (int u = 0; u < VE; ++u) to[u] = f[u];
+    }
+};
+
+// Stores an access at `to`, of which the columns c .. are those in the row.
+template <typename T, int LIE>
+__device__ __forceinline__ void put(const float* f, char* to, int c, int cols) {
+    constexpr int VE = kVe<T, LIE>;
+    float t[VE];
+#pragma unroll
+    for (int u = 0; u < VE; ++u) t[u] = f[u];
+    if (whole<T, LIE>(c, cols)) {
+        Vec<T, VE> v;
+        v.set(t);
+        v.store(reinterpret_cast<T*>(to));
+    } else if (LIE == kOff) {
+#pragma unroll
+        for (int u = 0; u < VE; ++u)
+            if (c + u >= 0 && c + u < cols) reinterpret_cast<T*>(to)[u] = from_f32<T>(t[u]);
+    }
 }
 
-// Rows too long for a CTA's registers: the same three passes, re-reading the
-// row (h, where there is a residual) from the caches.
-template <typename T>
+// VE parameters from column c on; those outside the row are `fill`.
+template <typename T, int LIE>
+__device__ __forceinline__ void params(float* to, const void* p, bool f32, int c, int cols, float fill) {
+    constexpr int VE = kVe<T, LIE>;
+    float t[VE];
+#pragma unroll
+    for (int u = 0; u < VE; ++u) t[u] = fill;
+    if (p && LIE != kOff && c < cols) {
+        load_param<T, VE>(t, p, f32, c);
+    } else if (p && LIE == kOff) {
+#pragma unroll
+        for (int u = 0; u < VE; ++u)
+            if (c + u >= 0 && c + u < cols) {
+                float one[1];
+                load_param<T, 1>(one, p, f32, c + u);
+                t[u] = one[0];
+            }
+    }
+#pragma unroll
+    for (int u = 0; u < VE; ++u) to[u] = t[u];
+}
+
+__device__ __forceinline__ float half_of(float2 v, int second) { return second ? v.y : v.x; }
+
+constexpr int kGroupThreads = 128;  // CTA of a kernel whose rows take a group of lanes
+constexpr int kRowThreads = 512;    // largest CTA of a kernel whose rows take the CTA
+
+// Resident CTAs of C threads by the columns of a thread: with up to eight, 64
+// registers a thread are enough, 80 for groups.
+constexpr int ctas_for(int elems, int C, bool group) { return (elems > 8 ? 512 : group ? 768 : 1024) / C; }
+
+template <typename T, int LIE, int V, int S, int C, bool GROUP>
+__global__ void __launch_bounds__(C, ctas_for(V * kVe<T, LIE>, C, GROUP))
+    norm_kernel(NormParams p, int L) {
+    extern __shared__ uint4 s_ring[];
+    static_assert(kRowThreads == 16 * 32, "half a warp holds the warps' sums");
+    __shared__ float2 s_part[2][16];
+    __shared__ float2 s_count[16];  // a warp's columns, and 1 over that
+    using R = Ring<T, LIE, V, S, 2, C, GROUP>;
+    constexpr int VE = R::VE;
+    const R ring(s_ring);
+    const int lane = GROUP ? threadIdx.x & (L - 1) : threadIdx.x;
+    const int per = GROUP ? kGroupThreads / L : 1;
+    const int hop = gridDim.x * per, rows = static_cast<int>(p.rows);
+    const int row0 = blockIdx.x * per;
+    int row = row0 + (GROUP ? threadIdx.x / L : 0);
+    // rows of this thread's group or CTA that are still to be fetched, and
+    // rounds of the CTA
+    int left = row < rows ? (rows - row - 1) / hop + 1 : 0;
+    int rounds = (rows - row0 - 1) / hop + 1;
+    // columns of this thread's first access that belong to the row before
+    const int se = LIE == kOff ? (row % VE) * (p.cols % VE) % VE : 0;
+    const char *x = static_cast<const char*>(p.x), *res = static_cast<const char*>(p.residual);
+    const float inv_n = 1.0f / static_cast<float>(p.cols);
+    auto col = [&](int i) { return (i * L + lane) * VE - se; };
+    auto has = [&](int i) { return col(i) < p.cols; };
+    // byte offset of this thread's columns in the present row and in the row
+    // that is fetched, and from a row to its next one
+    const int64_t step = static_cast<int64_t>(hop) * p.cols * sizeof(T);
+    int64_t at = (static_cast<int64_t>(row) * p.cols + lane * VE - se) * static_cast<int>(sizeof(T)), far = at;
+
+    auto fetch = [&](uint32_t st) {
+        if (left > 0) {
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (has(i)) {
+                    ring.fetch(st, 0, i, x + far + i * L * R::kBytes, col(i), p.cols);
+                    if (res) ring.fetch(st, 1, i, res + far + i * L * R::kBytes, col(i), p.cols);
+                }
+        }
+        ptx::cp_async_commit();
+        far += step;
+        --left;
+    };
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        if (!has(i)) {
+            ring.clear(0, i);
+            if (res) ring.clear(1, i);
+        }
+#pragma unroll
+    for (int s = 0; s < S - 1; ++s) fetch(s * R::kStage);
+
+    constexpr int E = V * VE, P = (E + 1) / 2;  // a thread's columns, in pairs
+    float w[2 * P], b[2 * P];
+    if (E & 1) w[E] = b[E] = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        params<T, LIE>(w + i * VE, p.weight, p.w_f32, col(i), p.cols, 1.f);
+        params<T, LIE>(b + i * VE, p.bias, p.w_f32, col(i), p.cols, 0.f);
+    }
+    float mine = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) mine += static_cast<float>(max(0, min(col(i) + VE, p.cols) - max(col(i), 0)));
+    if (!GROUP) {
+        const float n = lanes_sum(mine, 32);
+        if ((threadIdx.x & 31) == 0) s_count[threadIdx.x >> 5] = make_float2(n, n > 0.f ? 1.f / n : 0.f);
+        __syncthreads();
+    }
+    const int nw = blockDim.x >> 5, wl = threadIdx.x & 31;
+    const float warp_inv = GROUP ? inv_n : s_count[threadIdx.x >> 5].y;
+    const float2 count = !GROUP && (wl & 15) < nw ? s_count[wl & 15] : make_float2(0.f, 0.f);
+
+    uint32_t st = 0, ahead = (S - 1) * R::kStage;
+    int turn = 0;
+    // every thread of the CTA makes the same rounds (barriers, shuffles)
+    for (; rounds > 0; --rounds) {
+        const bool live = !GROUP || row < rows;
+        fetch(ahead);
+        ptx::cp_async_wait<S - 1>();
+        float f[2 * P];
+        if (E & 1) f[E] = 0.f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int64_t a = at + i * L * R::kBytes;
+            ring.take(f + i * VE, st, 0, i, x + a, col(i), p.cols, live);
+            if (res) {
+                float r[VE];
+                ring.take(r, st, 1, i, res + a, col(i), p.cols, live);
+#pragma unroll
+                for (int u = 0; u < VE; ++u) r[u] += f[i * VE + u];
+                Vec<T, VE> h;
+                h.set(r);
+                h.get(r);  // as it is stored
+#pragma unroll
+                for (int u = 0; u < VE; ++u) f[i * VE + u] = r[u];
+                if (live && has(i)) put<T, LIE>(f + i * VE, static_cast<char*>(p.h) + a, col(i), p.cols);
+            }
+        }
+        float2 s2 = both(0.f);
+#pragma unroll
+        for (int k = 0; k < P; ++k) s2 = add2(s2, make_float2(f[2 * k], f[2 * k + 1]));
+        // squared distances from the mean of the group or the warp
+        const float s = lanes_sum(s2.x + s2.y, GROUP ? L : 32);
+        float mean = s * warp_inv, q = 0.f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            if (whole<T, LIE>(col(i), p.cols)) {
+#pragma unroll
+                for (int u = 0; u < VE; ++u) q += (f[i * VE + u] - mean) * (f[i * VE + u] - mean);
+            } else if (LIE == kOff) {
+#pragma unroll
+                for (int u = 0; u < VE; ++u)
+                    if (col(i) + u >= 0 && col(i) + u < p.cols) q += (f[i * VE + u] - mean) * (f[i * VE + u] - mean);
+            }
+        }
+        q = lanes_sum(q, GROUP ? L : 32);
+        if (!GROUP) {
+            // the warps' sums joined: around the row's mean a warp's squares
+            // are its own and its columns times the means' distance squared.
+            // Two sets in turn: a set is written again only after the barrier
+            // of the row between.
+            float2* part = s_part[turn];
+            if (wl == 0) part[threadIdx.x >> 5] = make_float2(s, q);
+            __syncthreads();
+            const float2 a = (wl & 15) < nw ? part[wl & 15] : make_float2(0.f, 0.f);
+            mean = lanes_sum(a.x, 16) * inv_n;
+            const float d = a.x * count.y - mean;
+            q = lanes_sum(count.x > 0.f ? a.y + count.x * d * d : 0.f, 16);
+        }
+        const float rstd = 1.0f / sqrtf(q * inv_n + p.eps);
+        if (live && lane == 0) {
+            p.mean[row] = mean;
+            p.rstd[row] = rstd;
+        }
+#pragma unroll
+        for (int k = 0; k < P; ++k) {
+            const float2 d = mul2(add2(make_float2(f[2 * k], f[2 * k + 1]), both(-mean)), both(rstd));
+            const float2 o = fma2(d, make_float2(w[2 * k], w[2 * k + 1]), make_float2(b[2 * k], b[2 * k + 1]));
+            f[2 * k] = o.x;
+            f[2 * k + 1] = o.y;
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (live && has(i))
+                put<T, LIE>(f + i * VE, static_cast<char*>(p.y) + at + i * L * R::kBytes, col(i), p.cols);
+        row += hop;
+        at += step;
+        turn ^= 1;
+        st = R::next(st);
+        ahead = R::next(ahead);
+    }
+}
+
+// Rows too long for a CTA's registers: three passes, re-reading the row (h,
+// where there is a residual) from the caches.
+template <typename T, int VE>
 __global__ void __launch_bounds__(1024) norm_long_kernel(NormParams p) {
     __shared__ float s_part[2][32];
     const int64_t base = static_cast<int64_t>(blockIdx.x) * p.cols;
     const T* x = static_cast<const T*>(p.x) + base;
     const T* r = p.residual ? static_cast<const T*>(p.residual) + base : nullptr;
     T* ho = static_cast<T*>(p.h) + base;
-    float s = 0.f;
-    for (int c = threadIdx.x; c < p.cols; c += blockDim.x) {
-        T v = x[c];
-        if (r) ho[c] = v = from_f32<T>(to_f32(v) + to_f32(r[c]));
-        s += to_f32(v);
-    }
     const T* h = r ? ho : x;  // each thread reads back what it wrote itself
+    T* y = static_cast<T*>(p.y) + base;
+    const int hop = blockDim.x * VE, first = threadIdx.x * VE;
+    Vec<T, VE> v;
+    float f[VE], s = 0.f;
+    for (int c = first; c < p.cols; c += hop) {
+        v.load(x + c);
+        v.get(f);
+        if (r) {
+            float g[VE];
+            v.load(r + c);
+            v.get(g);
+#pragma unroll
+            for (int u = 0; u < VE; ++u) f[u] += g[u];
+            v.set(f);
+            v.store(ho + c);
+            v.get(f);
+        }
+#pragma unroll
+        for (int u = 0; u < VE; ++u) s += f[u];
+    }
     const float inv_n = 1.0f / static_cast<float>(p.cols);
     const float mean = block_sum(s, s_part[0]) * inv_n;
     float q = 0.f;
-    for (int c = threadIdx.x; c < p.cols; c += blockDim.x) {
-        const float d = to_f32(h[c]) - mean;
-        q += d * d;
+    for (int c = first; c < p.cols; c += hop) {
+        v.load(h + c);
+        v.get(f);
+#pragma unroll
+        for (int u = 0; u < VE; ++u) q += (f[u] - mean) * (f[u] - mean);
     }
     const float rstd = 1.0f / sqrtf(block_sum(q, s_part[1]) * inv_n + p.eps);
     if (threadIdx.x == 0) {
         p.mean[blockIdx.x] = mean;
         p.rstd[blockIdx.x] = rstd;
     }
-    T* y = static_cast<T*>(p.y) + base;
-    for (int c = threadIdx.x; c < p.cols; c += blockDim.x) {
-        float w[1] = {1.f}, b[1] = {0.f};
-        if (p.weight) load_param<T, 1>(w, p.weight, p.w_f32, c);
-        if (p.bias) load_param<T, 1>(b, p.bias, p.w_f32, c);
-        y[c] = from_f32<T>((to_f32(h[c]) - mean) * rstd * w[0] + b[0]);
+    for (int c = first; c < p.cols; c += hop) {
+        float w[VE], b[VE];
+#pragma unroll
+        for (int u = 0; u < VE; ++u) w[u] = 1.f, b[u] = 0.f;
+        if (p.weight) load_param<T, VE>(w, p.weight, p.w_f32, c);
+        if (p.bias) load_param<T, VE>(b, p.bias, p.w_f32, c);
+        v.load(h + c);
+        v.get(f);
+#pragma unroll
+        for (int u = 0; u < VE; ++u) f[u] = (f[u] - mean) * rstd * w[u] + b[u];
+        v.set(f);
+        v.store(y + c);
     }
-}
-
-int pow2_at_least(int v) {
-    int r = 1;
-    while (r < v) r <<= 1;
-    return r;
-}
-
-template <typename T, int VE, bool WARP>
-cudaError_t launch_norm_v(const NormParams& p, int L, int V, cudaStream_t st) {
-    const int threads = WARP ? kWarpRowThreads : L;
-    const int rows_per_cta = WARP ? kWarpRowThreads / L : 1;
-    const dim3 grid(static_cast<unsigned>((p.rows + rows_per_cta - 1) / rows_per_cta));
-    auto go = [&](auto kernel) { return launch_kernel(kernel, grid, dim3(threads), 0, st, false, p, L); };
-    if (V <= 1) return go(norm_kernel<T, VE, 1, WARP>);
-    if (V <= 2) return go(norm_kernel<T, VE, 2, WARP>);
-    if (V <= 4) return go(norm_kernel<T, VE, 4, WARP>);
-    if (V <= 8) return go(norm_kernel<T, VE, 8, WARP>);
-    return go(norm_kernel<T, VE, 16, WARP>);
-}
-
-template <typename T, int VE>
-cudaError_t launch_norm_t(const NormParams& p, cudaStream_t st) {
-    const int nvec = p.cols / VE;
-    if (nvec <= 32 * 16) {
-        const int L = nvec >= 32 ? 32 : pow2_at_least(nvec);
-        return launch_norm_v<T, VE, true>(p, L, (nvec + L - 1) / L, st);
-    }
-    if (nvec <= 1024 * 4) {
-        const int L = ((nvec + 3) / 4 + 31) & ~31;
-        return launch_norm_v<T, VE, false>(p, L, 4, st);
-    }
-    return launch_kernel(norm_long_kernel<T>, dim3(static_cast<unsigned>(p.rows)), dim3(1024), 0, st, false, p);
 }
 
 // ------------------------------------------------------------ gradient
 // With xh = (h - mean) rstd and a = dy w:
 //   dx = rstd (a - mean(a) - xh mean(a xh)) (+ dh, the residual stream's)
 //   dw = sum over rows of dy xh,  db = sum over rows of dy
-// A CTA walks over rows; a thread owns the same columns of each, so its sums
-// of dy xh and dy stay in registers and leave once, as one row of partial
-// sums per CTA; a second launch adds those in a fixed order.
-constexpr int kGradThreads = 256;  // warp rows
-
-template <typename T, int VE, int V, bool WARP>
-__global__ void __launch_bounds__(WARP ? kGradThreads : 1024, 1) norm_grad_kernel(NormGradParams p, int L) {
-    __shared__ float s_part[2][2][32];
-    extern __shared__ float s_sum[];  // WARP: [2][cols]
-    const int lane = WARP ? threadIdx.x & (L - 1) : threadIdx.x;
-    const int rows_per_cta = WARP ? kGradThreads / L : 1;
-    const int nvec = p.cols / VE;
+// A thread's column sums leave once, as one row of partial sums per CTA; a
+// second launch adds those in a fixed order.
+template <typename T, int LIE, int V, int S, int C, bool GROUP>
+__global__ void __launch_bounds__(C, ctas_for(V * kVe<T, LIE>, C, GROUP))
+    norm_grad_kernel(NormGradParams p, int L) {
+    extern __shared__ uint4 s_ring[];
+    static_assert(kRowThreads == 16 * 32, "half a warp holds the warps' sums");
+    __shared__ float s_part[2][2][16];
+    using R = Ring<T, LIE, V, S, 3, C, GROUP>;
+    constexpr int VE = R::VE;
+    const R ring(s_ring);
+    const int lane = GROUP ? threadIdx.x & (L - 1) : threadIdx.x;
+    const int per = GROUP ? kGroupThreads / L : 1;
+    const int hop = gridDim.x * per, rows = static_cast<int>(p.rows);
+    const int row0 = blockIdx.x * per;
+    int row = row0 + (GROUP ? threadIdx.x / L : 0);
+    // rows of this thread's group or CTA that are still to be fetched, and
+    // rounds of the CTA
+    int left = row < rows ? (rows - row - 1) / hop + 1 : 0;
+    int rounds = (rows - row0 - 1) / hop + 1;
+    // columns of this thread's first access that belong to the row before
+    const int se = LIE == kOff ? (row % VE) * (p.cols % VE) % VE : 0;
+    const char *h = static_cast<const char*>(p.h), *dy = static_cast<const char*>(p.dy);
+    const char* dh = static_cast<const char*>(p.dh);
     const float inv_n = 1.0f / static_cast<float>(p.cols);
-    float aw[V * VE], ab[V * VE];
+    const int nw = blockDim.x >> 5, wl = threadIdx.x & 31;
+    const uint32_t stat = ring.stats + (GROUP ? threadIdx.x / L : threadIdx.x >> 5) * 8;
+    auto col = [&](int i) { return (i * L + lane) * VE - se; };
+    auto has = [&](int i) { return col(i) < p.cols; };
+    const int64_t step = static_cast<int64_t>(hop) * p.cols * sizeof(T);
+    int64_t at = (static_cast<int64_t>(row) * p.cols + lane * VE - se) * static_cast<int>(sizeof(T)), far = at;
+    const float *far_mean = p.mean + row, *far_rstd = p.rstd + row;
+
+    auto fetch = [&](uint32_t st) {
+        if (left > 0) {
 #pragma unroll
-    for (int i = 0; i < V * VE; ++i) aw[i] = ab[i] = 0.f;
-    int turn = 0;
-    for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * rows_per_cta; r0 < p.rows;
-         r0 += static_cast<int64_t>(gridDim.x) * rows_per_cta) {
-        const int64_t row = WARP ? r0 + threadIdx.x / L : r0;
-        const bool live = row < p.rows;
-        const int64_t base = row * p.cols;
-        const float mean = live ? p.mean[row] : 0.f, rstd = live ? p.rstd[row] : 0.f;
-        Vec<T, VE> x[V], dy[V];
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-            if (live && i * L + lane < nvec) {
-                const int64_t c = base + static_cast<int64_t>(i * L + lane) * VE;
-                x[i] = load_vec<T, VE>(static_cast<const T*>(p.h) + c);
-                dy[i] = load_vec<T, VE>(static_cast<const T*>(p.dy) + c);
-            }
-        float sa = 0.f, sx = 0.f;
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-            if (live && i * L + lane < nvec) {
-                float w[VE];
-#pragma unroll
-                for (int u = 0; u < VE; ++u) w[u] = 1.f;
-                if (p.weight) load_param<T, VE>(w, p.weight, p.w_f32, static_cast<int64_t>(i * L + lane) * VE);
-#pragma unroll
-                for (int u = 0; u < VE; ++u) {
-                    const float g = to_f32(dy[i].v[u]), xh = (to_f32(x[i].v[u]) - mean) * rstd, a = g * w[u];
-                    sa += a;
-                    sx += a * xh;
-                    aw[i * VE + u] += g * xh;
-                    ab[i * VE + u] += g;
+            for (int i = 0; i < V; ++i)
+                if (has(i)) {
+                    ring.fetch(st, 0, i, h + far + i * L * R::kBytes, col(i), p.cols);
+                    ring.fetch(st, 1, i, dy + far + i * L * R::kBytes, col(i), p.cols);
+                    if (dh) ring.fetch(st, 2, i, dh + far + i * L * R::kBytes, col(i), p.cols);
                 }
+            // the row's statistics, once for the warp or the group
+            if ((GROUP ? lane : wl) == 0) {
+                ptx::cp_async_4(stat + st, far_mean);
+                ptx::cp_async_4(stat + st + 4, far_rstd);
             }
-        if (WARP) {
+        }
+        ptx::cp_async_commit();
+        far += step;
+        --left;
+        far_mean += hop;
+        far_rstd += hop;
+    };
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        if (!has(i)) {
+            ring.clear(0, i);
+            ring.clear(1, i);
+            if (dh) ring.clear(2, i);
+        }
+#pragma unroll
+    for (int s = 0; s < S - 1; ++s) fetch(s * R::kStage);
+
+    constexpr int E = V * VE, P = (E + 1) / 2;  // a thread's columns, in pairs
+    float w[2 * P];
+    float2 aw[P], ab[P];
+#pragma unroll
+    for (int k = 0; k < P; ++k) aw[k] = ab[k] = both(0.f);
+    if (E & 1) w[E] = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) params<T, LIE>(w + i * VE, p.weight, p.w_f32, col(i), p.cols, 1.f);
+
+    uint32_t st = 0, ahead = (S - 1) * R::kStage;
+    int turn = 0;
+    for (; rounds > 0; --rounds) {
+        const bool live = !GROUP || row < rows;
+        fetch(ahead);
+        ptx::cp_async_wait<S - 1>();
+        __syncwarp();
+        const float mean = live ? __uint_as_float(ptx::ld_shared_4(stat + st)) : 0.f;
+        const float rstd = live ? __uint_as_float(ptx::ld_shared_4(stat + st + 4)) : 0.f;
+        // d = h - mean and a = rstd dy w of the thread's columns; columns that
+        // it does not have are zero and add nothing
+        float f[2 * P], g[2 * P];
+        if (E & 1) f[E] = g[E] = 0.f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            ring.take(f + i * VE, st, 0, i, h + at + i * L * R::kBytes, col(i), p.cols, live);
+            ring.take(g + i * VE, st, 1, i, dy + at + i * L * R::kBytes, col(i), p.cols, live);
+        }
+        if (GROUP && !live) {  // what an earlier row left in the slots
+#pragma unroll
+            for (int k = 0; k < 2 * P; ++k) f[k] = g[k] = 0.f;
+        }
+        float2 d[P], a[P], sa2 = both(0.f), sx2 = both(0.f);
+#pragma unroll
+        for (int k = 0; k < P; ++k) {
+            const float2 g2 = make_float2(g[2 * k], g[2 * k + 1]);
+            const float2 gr = mul2(g2, both(rstd));
+            d[k] = add2(make_float2(f[2 * k], f[2 * k + 1]), both(-mean));
+            a[k] = mul2(gr, make_float2(w[2 * k], w[2 * k + 1]));
+            sa2 = add2(sa2, a[k]);
+            sx2 = fma2(a[k], d[k], sx2);
+            aw[k] = fma2(gr, d[k], aw[k]);
+            ab[k] = add2(ab[k], g2);
+        }
+        // sums of a and of a d: the halves of the warp take one each after the
+        // first exchange
+        float sa = sa2.x + sa2.y, sx = sx2.x + sx2.y;
+        if (GROUP) {
             sa = lanes_sum(sa, L);
             sx = lanes_sum(sx, L);
         } else {
-            // two sets of sums in turn: a set is written again only after the
-            // barrier of the row between
-            sa = lanes_sum(sa, 32);
-            sx = lanes_sum(sx, 32);
-            if ((threadIdx.x & 31) == 0) {
-                s_part[turn][0][threadIdx.x >> 5] = sa;
-                s_part[turn][1][threadIdx.x >> 5] = sx;
-            }
+            const bool upper = wl >= 16;
+            float s = upper ? sx : sa;
+            s += __shfl_xor_sync(0xffffffffu, upper ? sa : sx, 16);
+            s = lanes_sum(s, 16);
+            // two sets in turn: a set is written again only after the barrier
+            // of the row between
+            float* part = s_part[turn][upper];
+            if ((wl & 15) == 0) part[threadIdx.x >> 5] = s;
             __syncthreads();
-            const int nw = blockDim.x >> 5, wl = threadIdx.x & 31;
-            sa = lanes_sum(wl < nw ? s_part[turn][0][wl] : 0.f, 32);
-            sx = lanes_sum(wl < nw ? s_part[turn][1][wl] : 0.f, 32);
-            turn ^= 1;
+            s = lanes_sum((wl & 15) < nw ? part[wl & 15] : 0.f, 16);
+            const float o = __shfl_xor_sync(0xffffffffu, s, 16);
+            sa = upper ? o : s;
+            sx = upper ? s : o;
         }
-        const float ma = sa * inv_n, mx = sx * inv_n;
+        // dx = a - mean(a) - d rstd^2 mean(a d)
+        const float2 ca = both(-sa * inv_n), cx = both(-sx * inv_n * rstd * rstd);
 #pragma unroll
-        for (int i = 0; i < V; ++i)
-            if (live && i * L + lane < nvec) {
-                const int64_t wc = static_cast<int64_t>(i * L + lane) * VE;
-                float w[VE];
+        for (int k = 0; k < P; ++k) {
+            const float2 o = add2(fma2(d[k], cx, a[k]), ca);
+            f[2 * k] = o.x;
+            f[2 * k + 1] = o.y;
+        }
 #pragma unroll
-                for (int u = 0; u < VE; ++u) w[u] = 1.f;
-                if (p.weight) load_param<T, VE>(w, p.weight, p.w_f32, wc);
-                float o[VE];
+        for (int i = 0; i < V; ++i) {
+            if (dh) {
+                float e[VE];
+                ring.take(e, st, 2, i, dh + at + i * L * R::kBytes, col(i), p.cols, live);
 #pragma unroll
-                for (int u = 0; u < VE; ++u) {
-                    const float xh = (to_f32(x[i].v[u]) - mean) * rstd;
-                    o[u] = rstd * (to_f32(dy[i].v[u]) * w[u] - ma - xh * mx);
-                }
-                if (p.dh) {
-                    const Vec<T, VE> d = load_vec<T, VE>(static_cast<const T*>(p.dh) + base + wc);
-#pragma unroll
-                    for (int u = 0; u < VE; ++u) o[u] += to_f32(d.v[u]);
-                }
-                Vec<T, VE> out;
-#pragma unroll
-                for (int u = 0; u < VE; ++u) out.v[u] = from_f32<T>(o[u]);
-                store_vec<T, VE>(static_cast<T*>(p.dx) + base + wc, out);
+                for (int u = 0; u < VE; ++u) f[i * VE + u] += e[u];
             }
+            if (live && has(i))
+                put<T, LIE>(f + i * VE, static_cast<char*>(p.dx) + at + i * L * R::kBytes, col(i), p.cols);
+        }
+        row += hop;
+        at += step;
+        turn ^= 1;
+        st = R::next(st);
+        ahead = R::next(ahead);
     }
     if (!p.partial) return;
     float* part = p.partial + static_cast<int64_t>(blockIdx.x) * 2 * p.cols;
-    if (!WARP) {
+    if (!GROUP) {
 #pragma unroll
         for (int i = 0; i < V; ++i)
-            if (i * L + lane < nvec) {
-                const int c = (i * L + lane) * VE;
+            if (has(i)) {
 #pragma unroll
                 for (int u = 0; u < VE; ++u) {
-                    part[c + u] = aw[i * VE + u];
-                    part[p.cols + c + u] = ab[i * VE + u];
+                    if (LIE == kOff && (col(i) + u < 0 || col(i) + u >= p.cols)) continue;
+                    part[col(i) + u] = half_of(aw[(i * VE + u) / 2], (i * VE + u) & 1);
+                    part[p.cols + col(i) + u] = half_of(ab[(i * VE + u) / 2], (i * VE + u) & 1);
                 }
             }
-        return;
-    }
-    // the warp's groups, then the CTA's warps one after another
+    } else {
+        // the warp's groups by shuffles, then the warps one after another; off
+        // the grid the groups hold different columns, so all one after another
+        // (the ring is free: no row is on its way)
+        float* s_sum = reinterpret_cast<float*>(s_ring);
+        constexpr bool kOne = LIE == kOff;
+        if (!kOne) {
 #pragma unroll
-    for (int i = 0; i < V * VE; ++i)
-        for (int o = 16; o >= L; o >>= 1) {
-            aw[i] += __shfl_xor_sync(0xffffffffu, aw[i], o);
-            ab[i] += __shfl_xor_sync(0xffffffffu, ab[i], o);
-        }
-    const bool first = (threadIdx.x & 31) < L;
-    for (int wi = 0; wi < kGradThreads / 32; ++wi) {
-        if (first && static_cast<int>(threadIdx.x >> 5) == wi) {
-#pragma unroll
-            for (int i = 0; i < V; ++i)
-                if (i * L + lane < nvec) {
-                    const int c = (i * L + lane) * VE;
-#pragma unroll
-                    for (int u = 0; u < VE; ++u) {
-                        s_sum[c + u] = (wi ? s_sum[c + u] : 0.f) + aw[i * VE + u];
-                        s_sum[p.cols + c + u] = (wi ? s_sum[p.cols + c + u] : 0.f) + ab[i * VE + u];
-                    }
+            for (int k = 0; k < P; ++k)
+                for (int o = 16; o >= L; o >>= 1) {
+                    aw[k].x += __shfl_xor_sync(0xffffffffu, aw[k].x, o);
+                    aw[k].y += __shfl_xor_sync(0xffffffffu, aw[k].y, o);
+                    ab[k].x += __shfl_xor_sync(0xffffffffu, ab[k].x, o);
+                    ab[k].y += __shfl_xor_sync(0xffffffffu, ab[k].y, o);
                 }
         }
+        ptx::cp_async_wait<0>();
+        const int turns = kOne ? C / L : C / 32, my_turn = kOne ? threadIdx.x / L : threadIdx.x >> 5;
+        for (int t = 0; t < turns; ++t) {
+            __syncthreads();
+            if (my_turn == t && (kOne || wl < L)) {
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+                    if (has(i)) {
+#pragma unroll
+                        for (int u = 0; u < VE; ++u) {
+                            const int c = col(i) + u, k = (i * VE + u) / 2;
+                            if (LIE == kOff && (c < 0 || c >= p.cols)) continue;
+                            s_sum[c] = (t ? s_sum[c] : 0.f) + half_of(aw[k], (i * VE + u) & 1);
+                            s_sum[p.cols + c] = (t ? s_sum[p.cols + c] : 0.f) + half_of(ab[k], (i * VE + u) & 1);
+                        }
+                    }
+            }
+        }
         __syncthreads();
+        for (int c = threadIdx.x; c < 2 * p.cols; c += kGroupThreads) part[c] = s_sum[c];
     }
-    for (int c = threadIdx.x; c < 2 * p.cols; c += kGradThreads) part[c] = s_sum[c];
+    ptx::pdl_launch_dependents();
 }
 
 // Long rows: dx alone, the row re-read from the caches.
-template <typename T>
+template <typename T, int VE>
 __global__ void __launch_bounds__(1024) norm_grad_long_kernel(NormGradParams p) {
     __shared__ float s_part[2][32];
     const int64_t row = blockIdx.x, base = row * p.cols;
-    const T* x = static_cast<const T*>(p.h) + base;
-    const T* dy = static_cast<const T*>(p.dy) + base;
+    const T *x = static_cast<const T*>(p.h) + base, *dy = static_cast<const T*>(p.dy) + base;
     const float mean = p.mean[row], rstd = p.rstd[row], inv_n = 1.0f / static_cast<float>(p.cols);
-    float sa = 0.f, sx = 0.f;
-    for (int c = threadIdx.x; c < p.cols; c += blockDim.x) {
-        float w[1] = {1.f};
-        if (p.weight) load_param<T, 1>(w, p.weight, p.w_f32, c);
-        const float a = to_f32(dy[c]) * w[0];
-        sa += a;
-        sx += a * (to_f32(x[c]) - mean) * rstd;
+    const int hop = blockDim.x * VE, first = threadIdx.x * VE;
+    Vec<T, VE> v;
+    float f[VE], g[VE], w[VE], sa = 0.f, sx = 0.f;
+#pragma unroll
+    for (int u = 0; u < VE; ++u) w[u] = 1.f;
+    // xh in f, dy w in g
+    auto load = [&](int c) {
+        v.load(x + c);
+        v.get(f);
+        v.load(dy + c);
+        v.get(g);
+        if (p.weight) load_param<T, VE>(w, p.weight, p.w_f32, c);
+#pragma unroll
+        for (int u = 0; u < VE; ++u) f[u] = (f[u] - mean) * rstd, g[u] *= w[u];
+    };
+    for (int c = first; c < p.cols; c += hop) {
+        load(c);
+#pragma unroll
+        for (int u = 0; u < VE; ++u) sa += g[u], sx += g[u] * f[u];
     }
     const float ma = block_sum(sa, s_part[0]) * inv_n, mx = block_sum(sx, s_part[1]) * inv_n;
-    for (int c = threadIdx.x; c < p.cols; c += blockDim.x) {
-        float w[1] = {1.f};
-        if (p.weight) load_param<T, 1>(w, p.weight, p.w_f32, c);
-        const float xh = (to_f32(x[c]) - mean) * rstd;
-        float o = rstd * (to_f32(dy[c]) * w[0] - ma - xh * mx);
-        if (p.dh) o += to_f32(static_cast<const T*>(p.dh)[base + c]);
-        static_cast<T*>(p.dx)[base + c] = from_f32<T>(o);
+    for (int c = first; c < p.cols; c += hop) {
+        load(c);
+#pragma unroll
+        for (int u = 0; u < VE; ++u) f[u] = rstd * (g[u] - ma - f[u] * mx);
+        if (p.dh) {
+            v.load(static_cast<const T*>(p.dh) + base + c);
+            v.get(g);
+#pragma unroll
+            for (int u = 0; u < VE; ++u) f[u] += g[u];
+        }
+        v.set(f);
+        v.store(static_cast<T*>(p.dx) + base + c);
     }
 }
 
 // Long rows: column sums of rows blockIdx.y, blockIdx.y + gridDim.y, ...
-template <typename T>
+template <typename T, int VE>
 __global__ void __launch_bounds__(256) norm_grad_cols_kernel(NormGradParams p) {
-    const int c = blockIdx.x * 256 + threadIdx.x;
+    const int c = (blockIdx.x * 256 + threadIdx.x) * VE;
     if (c >= p.cols) return;
-    float aw = 0.f, ab = 0.f;
+    float aw[VE], ab[VE];
+#pragma unroll
+    for (int u = 0; u < VE; ++u) aw[u] = ab[u] = 0.f;
     for (int64_t row = blockIdx.y; row < p.rows; row += gridDim.y) {
-        const float g = to_f32(static_cast<const T*>(p.dy)[row * p.cols + c]);
-        const float xh = (to_f32(static_cast<const T*>(p.h)[row * p.cols + c]) - p.mean[row]) * p.rstd[row];
-        aw += g * xh;
-        ab += g;
+        const float mean = p.mean[row], rstd = p.rstd[row];
+        Vec<T, VE> x, dy;
+        float f[VE], g[VE];
+        x.load(static_cast<const T*>(p.h) + row * p.cols + c);
+        dy.load(static_cast<const T*>(p.dy) + row * p.cols + c);
+        x.get(f);
+        dy.get(g);
+#pragma unroll
+        for (int u = 0; u < VE; ++u) {
+            aw[u] += g[u] * ((f[u] - mean) * rstd);
+            ab[u] += g[u];
+        }
     }
-    float* part = p.partial + static_cast<int64_t>(blockIdx.y) * 2 * p.cols;
-    part[c] = aw;
-    part[p.cols + c] = ab;
+    float* part = p.partial + static_cast<int64_t>(blockIdx.y) * 2 * p.cols + c;
+#pragma unroll
+    for (int u = 0; u < VE; ++u) part[u] = aw[u], part[p.cols + u] = ab[u];
 }
 
 // Column sums over the partial rows: 32 columns per CTA, 32 threads deep.
 __global__ void __launch_bounds__(1024) norm_grad_sum_kernel(NormGradParams p, int parts) {
     __shared__ float s[32][33];
+    ptx::pdl_wait();
     const int c = blockIdx.x * 32 + (threadIdx.x & 31), depth = threadIdx.x >> 5;
     float a = 0.f;
     if (c < 2 * p.cols)
@@ -371,76 +653,120 @@ __global__ void __launch_bounds__(1024) norm_grad_sum_kernel(NormGradParams p, i
     }
 }
 
-template <typename T, int VE, bool WARP>
-cudaError_t launch_norm_grad_v(const NormGradParams& p, int L, int V, int grid, cudaStream_t st) {
-    const int threads = WARP ? kGradThreads : L;
-    const size_t smem = WARP ? size_t(2) * p.cols * sizeof(float) : 0;
-    auto go = [&](auto kernel) { return launch_kernel(kernel, dim3(grid), dim3(threads), smem, st, false, p, L); };
-    if (V <= 1) return go(norm_grad_kernel<T, VE, 1, WARP>);
-    if (V <= 2) return go(norm_grad_kernel<T, VE, 2, WARP>);
-    if constexpr (VE * 4 <= 32)
-        if (V <= 4) return go(norm_grad_kernel<T, VE, 4, WARP>);
-    if constexpr (VE * 8 <= 32)
-        if (V <= 8) return go(norm_grad_kernel<T, VE, 8, WARP>);
-    if constexpr (VE * 16 <= 32)
-        if (V <= 16) return go(norm_grad_kernel<T, VE, 16, WARP>);
-    if constexpr (VE * 32 <= 32)
-        if (V <= 32) return go(norm_grad_kernel<T, VE, 32, WARP>);
-    return cudaErrorInvalidValue;
+int pow2_at_least(int v) {
+    int r = 1;
+    while (r < v) r <<= 1;
+    return r;
 }
 
-template <typename T, int VE>
+// Rows of nvec accesses: f(accesses per thread V, largest CTA C, whether a
+// group of lanes takes a row, lanes or threads per row); V = 0 for rows longer
+// than kRowThreads threads hold with at most E columns each.  G: accesses per
+// lane up to which a group of lanes takes a row; V0: accesses per thread that
+// a CTA starts with.
+template <int VE, int G, int V0, int E, typename F>
+cudaError_t by_row(int nvec, F f) {
+    auto go = [&](auto v, auto c) {
+        return f(v, c, std::false_type{}, ((nvec + v.value - 1) / v.value + 31) & ~31);
+    };
+    auto group = [&](auto v) {
+        return f(v, std::integral_constant<int, kGroupThreads>{}, std::true_type{},
+                 std::min(32, pow2_at_least(nvec)));
+    };
+    constexpr std::integral_constant<int, kRowThreads> kMost{};
+    constexpr std::integral_constant<int, V0> v0{};
+    if (nvec <= 32) return group(std::integral_constant<int, 1>{});
+    if constexpr (G >= 2)
+        if (nvec <= 64) return group(std::integral_constant<int, 2>{});
+    if (nvec <= 128 * V0) return go(v0, std::integral_constant<int, 128>{});
+    if (nvec <= 256 * V0) return go(v0, std::integral_constant<int, 256>{});
+    if (nvec <= kRowThreads * V0) return go(v0, kMost);
+    if constexpr (VE * V0 * 2 <= E)
+        if (nvec <= kRowThreads * V0 * 2) return go(std::integral_constant<int, V0 * 2>{}, kMost);
+    if constexpr (VE * V0 * 4 <= E)
+        if (nvec <= kRowThreads * V0 * 4) return go(std::integral_constant<int, V0 * 4>{}, kMost);
+    return f(std::integral_constant<int, 0>{}, kMost, std::false_type{}, 0);
+}
+
+// Stages of the gradient by the bytes of a thread and row: 64 bytes of three
+// tensors in 512 threads leave room for two.
+constexpr int stages_for(int bytes) { return bytes <= 32 ? 3 : 2; }
+
+// One launch over all rows, as many CTAs as are resident by the launch bounds
+// and the ring.
+template <typename R, int C, bool GROUP, typename P, typename K>
+cudaError_t launch_rows(K kernel, const P& p, int L, int ctas_per_sm, int max_ctas, int* ctas_out, cudaStream_t st) {
+    constexpr int kSmem = R::kEnd;
+    static_assert(kSmem <= 224 << 10, "more than an SM has");
+    const int threads = GROUP ? C : L;
+    ctas_per_sm = std::min(ctas_per_sm * C / threads, (224 << 10) / (kSmem + 2048));
+    const int64_t per = GROUP ? C / L : 1;
+    // a multiple of 8, as kOff asks, where a CTA takes more than one row
+    const int64_t ctas = std::min<int64_t>(
+        {(p.rows + per - 1) / per, int64_t(kSms) * std::max(1, ctas_per_sm), static_cast<int64_t>(max_ctas)});
+    static_assert(kSms % 8 == 0 && kNormMaxPartials % 8 == 0, "CTAs a multiple of 8");
+    if (kSmem > 46 << 10) {  // the default limit of 48 KB holds the static part too
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+        if (e != cudaSuccess) return e;
+    }
+    if (ctas_out) *ctas_out = static_cast<int>(ctas);
+    return launch_kernel(kernel, dim3(static_cast<unsigned>(ctas)), dim3(threads), kSmem, st, false, p, L);
+}
+
+// Elements of an access of the long rows' kernels.
+template <typename T, int LIE>
+constexpr int kLong = LIE == kGrid ? kFull<T> : 1;
+
+template <typename T, int LIE>
+cudaError_t launch_norm_t(const NormParams& p, cudaStream_t st) {
+    constexpr int VE = kVe<T, LIE>;
+    return by_row<VE, VE == 1 ? 1 : 2, VE == 1 ? 4 : 1, 16>(accesses<T, LIE>(p.cols), [&](auto v, auto c, auto group, int L) {
+        constexpr int V = v.value, C = c.value, S = 2;
+        if constexpr (V == 0)
+            return launch_kernel(norm_long_kernel<T, kLong<T, LIE>>, dim3(static_cast<unsigned>(p.rows)), dim3(1024), 0, st, false, p);
+        else
+            return launch_rows<Ring<T, LIE, V, S, 2, C, group.value>, C, group.value>(norm_kernel<T, LIE, V, S, C, group.value>, p, L,
+                                                                        ctas_for(V * VE, C, group.value), 1 << 30, nullptr, st);
+    });
+}
+
+template <typename T, int LIE>
 cudaError_t launch_norm_grad_t(const NormGradParams& p, cudaStream_t st) {
-    const int nvec = p.cols / VE;
+    constexpr int VE = kVe<T, LIE>;
     int parts = 0;
     cudaError_t e = cudaSuccess;
-    if (p.rows == 0) {
-        // no row: the sums are zero
-    } else if (p.cols <= 1024) {  // V * VE <= 32 with 32 lanes
-        const int L = nvec >= 32 ? 32 : pow2_at_least(nvec);
-        const int64_t ctas = (p.rows + kGradThreads / L - 1) / (kGradThreads / L);
-        parts = static_cast<int>(ctas < kNormMaxPartials ? ctas : kNormMaxPartials);
-        e = launch_norm_grad_v<T, VE, true>(p, L, (nvec + L - 1) / L, parts, st);
-    } else if (p.cols <= 8192) {  // V * VE <= 16 with up to 512 threads
-        constexpr int V = 16 / VE;
-        const int L = ((nvec + V - 1) / V + 31) & ~31;
-        parts = static_cast<int>(p.rows < kNormMaxPartials ? p.rows : kNormMaxPartials);
-        e = launch_norm_grad_v<T, VE, false>(p, L, V, parts, st);
-    } else {
-        // the column sums first: dx may take dy's place
-        parts = static_cast<int>(p.rows < 64 ? p.rows : 64);
-        if (p.partial)
-            e = launch_kernel(norm_grad_cols_kernel<T>, dim3((p.cols + 255) / 256, parts), dim3(256), 0, st, false, p);
-        if (e == cudaSuccess)
-            e = launch_kernel(norm_grad_long_kernel<T>, dim3(static_cast<unsigned>(p.rows)), dim3(1024), 0, st, false,
-                              p);
-    }
+    if (p.rows > 0)  // without rows the sums are zero
+        e = by_row<VE, VE == 1 ? 1 : 2, VE == 1 ? 4 : 2, 16>(accesses<T, LIE>(p.cols), [&](auto v, auto c, auto group, int L) {
+            constexpr int V = v.value, C = c.value, S = stages_for(V * VE * sizeof(T));
+            if constexpr (V == 0) {
+                // the column sums first: dx may take dy's place
+                constexpr int VL = kLong<T, LIE>;
+                parts = static_cast<int>(p.rows < 64 ? p.rows : 64);
+                cudaError_t r = cudaSuccess;
+                if (p.partial)
+                    r = launch_kernel(norm_grad_cols_kernel<T, VL>, dim3((p.cols / VL + 255) / 256, parts), dim3(256), 0,
+                                      st, false, p);
+                if (r != cudaSuccess) return r;
+                return launch_kernel(norm_grad_long_kernel<T, VL>, dim3(static_cast<unsigned>(p.rows)), dim3(1024), 0,
+                                     st, false, p);
+            } else {
+                return launch_rows<Ring<T, LIE, V, S, 3, C, group.value>, C, group.value>(
+                    norm_grad_kernel<T, LIE, V, S, C, group.value>, p, L, ctas_for(V * VE, C, group.value), kNormMaxPartials, &parts,
+                    st);
+            }
+        });
     if (e != cudaSuccess || !p.partial) return e;
-    return launch_kernel(norm_grad_sum_kernel, dim3((2 * p.cols + 31) / 32), dim3(1024), 0, st, false, p, parts);
+    return launch_kernel(norm_grad_sum_kernel, dim3((2 * p.cols + 31) / 32), dim3(1024), 0, st, true, p, parts);
 }
 
 }  // namespace
 
-cudaError_t launch_norm(const NormParams& p, int dtype, bool vec, cudaStream_t st) {
-    switch (dtype) {
-        case MOE_DTYPE_BF16:
-            return vec ? launch_norm_t<__nv_bfloat16, 8>(p, st) : launch_norm_t<__nv_bfloat16, 1>(p, st);
-        case MOE_DTYPE_F16:
-            return vec ? launch_norm_t<__half, 8>(p, st) : launch_norm_t<__half, 1>(p, st);
-        default:
-            return vec ? launch_norm_t<float, 4>(p, st) : launch_norm_t<float, 1>(p, st);
-    }
+cudaError_t launch_norm(const NormParams& p, int dtype, int lie, cudaStream_t st) {
+    return by_type(dtype, lie, [&](auto t, auto lie) { return launch_norm_t<decltype(t), lie.value>(p, st); });
 }
 
-cudaError_t launch_norm_grad(const NormGradParams& p, int dtype, bool vec, cudaStream_t st) {
-    switch (dtype) {
-        case MOE_DTYPE_BF16:
-            return vec ? launch_norm_grad_t<__nv_bfloat16, 8>(p, st) : launch_norm_grad_t<__nv_bfloat16, 1>(p, st);
-        case MOE_DTYPE_F16:
-            return vec ? launch_norm_grad_t<__half, 8>(p, st) : launch_norm_grad_t<__half, 1>(p, st);
-        default:
-            return vec ? launch_norm_grad_t<float, 4>(p, st) : launch_norm_grad_t<float, 1>(p, st);
-    }
+cudaError_t launch_norm_grad(const NormGradParams& p, int dtype, int lie, cudaStream_t st) {
+    return by_type(dtype, lie, [&](auto t, auto lie) { return launch_norm_grad_t<decltype(t), lie.value>(p, st); });
 }
 
 }  // namespace moe

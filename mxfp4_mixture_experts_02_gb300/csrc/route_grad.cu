@@ -59,7 +59,7 @@ cudaError_t launch_route_grad(const RouteGradParams& p, cudaStream_t st) {
     const size_t smem = size_t(kRgWarps) * ((p.Eg + 3) & ~3) * sizeof(float);  // at most 32 KB
     const int64_t ctas = (p.T + kRgWarps - 1) / kRgWarps;
     const bool vec = p.Eg % 4 == 0 && (reinterpret_cast<uintptr_t>(p.dlogits) & 15) == 0;
-    return launch_kernel(route_grad_kernel, dim3(static_cast<unsigned>(ctas < 152 * 6 ? ctas : 152 * 6)),
+    return launch_kernel(route_grad_kernel, dim3(static_cast<unsigned>(ctas < kSms * 6 ? ctas : kSms * 6)),
                          dim3(kRgWarps * 32), smem, st, false, p, vec ? 1 : 0);
 }
 

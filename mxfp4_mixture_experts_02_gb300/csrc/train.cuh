@@ -34,27 +34,127 @@ __device__ __forceinline__ __half from_f32<__half>(float v) {
     return __float2half_rn(v);
 }
 
-// N elements moved with one access of their whole size, at most 16 bytes: the
-// alignment that the entries check (sm_103a has 32-byte accesses, which the
-// compiler takes for a larger type and which fault on a 16-byte boundary).
-template <typename T, int N>
-struct alignas(sizeof(T) * N) Vec {
-    static_assert(sizeof(T) * N <= 16, "wider than the alignment that is checked");
-    T v[N];
-};
-
 // Elements of a 16-byte access.
 template <typename T>
 constexpr int kFull = 16 / static_cast<int>(sizeof(T));
 
+// N elements moved with one access of their whole size: one element, or 16
+// bytes kept as packed words (16-bit elements apart cost a register each).
+// Never wider: sm_103a has 32-byte accesses, which fault on the 16-byte
+// boundary that the entries check.
 template <typename T, int N>
-__device__ __forceinline__ Vec<T, N> load_vec(const T* p) {
-    return *reinterpret_cast<const Vec<T, N>*>(p);
+struct Vec {
+    static_assert(N == kFull<T>, "one element or 16 bytes");
+    uint4 w;
+    __device__ __forceinline__ void load(const T* p) { w = *reinterpret_cast<const uint4*>(p); }
+    __device__ __forceinline__ void store(T* p) const { *reinterpret_cast<uint4*>(p) = w; }
+    __device__ __forceinline__ void get(float (&f)[N]) const {
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (sizeof(T) == 4) {
+                f[i] = __uint_as_float(u[i]);
+            } else if constexpr (std::is_same_v<T, __nv_bfloat16>) {
+                f[2 * i] = __uint_as_float(u[i] << 16);
+                f[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+            } else {
+                const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&u[i]));
+                f[2 * i] = h.x;
+                f[2 * i + 1] = h.y;
+            }
+        }
+    }
+    // rounded to nearest even
+    __device__ __forceinline__ void set(const float (&f)[N]) {
+        uint32_t u[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (sizeof(T) == 4) {
+                u[i] = __float_as_uint(f[i]);
+            } else if constexpr (std::is_same_v<T, __nv_bfloat16>) {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+                u[i] = *reinterpret_cast<const uint32_t*>(&h);
+            } else {
+                const __half2 h = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+                u[i] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+        }
+        w = make_uint4(u[0], u[1], u[2], u[3]);
+    }
+};
+
+template <typename T>
+struct Vec<T, 1> {
+    T v;
+    __device__ __forceinline__ void load(const T* p) { v = *p; }
+    __device__ __forceinline__ void store(T* p) const { *p = v; }
+    __device__ __forceinline__ void get(float (&f)[1]) const { f[0] = to_f32(v); }
+    __device__ __forceinline__ void set(const float (&f)[1]) { v = from_f32<T>(f[0]); }
+};
+
+// Two fp32 operations in one instruction, each half rounded by itself.
+__device__ __forceinline__ uint64_t bits2(float2 a) {
+    return static_cast<uint64_t>(__float_as_uint(a.x)) | static_cast<uint64_t>(__float_as_uint(a.y)) << 32;
+}
+__device__ __forceinline__ float2 float2_of(uint64_t b) {
+    return make_float2(__uint_as_float(static_cast<uint32_t>(b)), __uint_as_float(static_cast<uint32_t>(b >> 32)));
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(bits2(a)), "l"(bits2(b)));
+    return float2_of(d);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(bits2(a)), "l"(bits2(b)));
+    return float2_of(d);
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(bits2(a)), "l"(bits2(b)), "l"(bits2(c)));
+    return float2_of(d);
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+// How rows lie in memory:
+//   kGrid    every row starts on the 16-byte grid
+//   kOff     the tensors start on the grid, their rows do not (a row length
+//            that is no multiple of 16 bytes); a thread takes a whole piece of
+//            the grid, and the pieces at the ends of a row reach over them
+//   kSingle  element by element, for tensors that start off the grid
+enum Lie { kGrid, kOff, kSingle };
+
+template <typename T, int LIE>
+constexpr int kVe = LIE == kSingle ? 1 : kFull<T>;
+
+// Accesses that a row takes, wherever it starts.
+template <typename T, int LIE>
+int accesses(int cols) {
+    constexpr int VE = kVe<T, LIE>;
+    return (cols + VE - 1 + (LIE == kOff ? VE - 1 : 0)) / VE;
 }
 
-template <typename T, int N>
-__device__ __forceinline__ void store_vec(T* p, const Vec<T, N>& v) {
-    *reinterpret_cast<Vec<T, N>*>(p) = v;
+// Elements of the row from element `first` on that lie before it in its first
+// piece of the grid.
+template <typename T, int LIE>
+__device__ __forceinline__ int before(int64_t first) {
+    return LIE == kOff ? static_cast<int>(first % kFull<T>) : 0;
+}
+
+// The columns c .. c + VE - 1 are all in the row.
+template <typename T, int LIE>
+__device__ __forceinline__ bool whole(int c, int cols) {
+    return LIE == kOff ? c >= 0 && c + kFull<T> <= cols : c < cols;
+}
+
+template <typename F>
+cudaError_t by_type(int dtype, int lie, F f) {
+    auto go = [&](auto t) {
+        if (lie == kGrid) return f(t, std::integral_constant<int, kGrid>{});
+        if (lie == kOff) return f(t, std::integral_constant<int, kOff>{});
+        return f(t, std::integral_constant<int, kSingle>{});
+    };
+    return dtype == MOE_DTYPE_BF16 ? go(__nv_bfloat16{}) : dtype == MOE_DTYPE_F16 ? go(__half{}) : go(float{});
 }
 
 // N parameters (a norm's weight or bias) from column c on, kept in 32 bits or
@@ -62,17 +162,20 @@ __device__ __forceinline__ void store_vec(T* p, const Vec<T, N>& v) {
 template <typename T, int N>
 __device__ __forceinline__ void load_param(float (&out)[N], const void* p, bool f32, int64_t c) {
     if (f32) {
-        constexpr int M = N < 4 ? N : 4;  // 16 bytes
+        constexpr int M = N < 4 ? N : 4;
 #pragma unroll
         for (int i = 0; i < N; i += M) {
-            const Vec<float, M> v = load_vec<float, M>(static_cast<const float*>(p) + c + i);
+            Vec<float, M> v;
+            float f[M];
+            v.load(static_cast<const float*>(p) + c + i);
+            v.get(f);
 #pragma unroll
-            for (int u = 0; u < M; ++u) out[i + u] = v.v[u];
+            for (int u = 0; u < M; ++u) out[i + u] = f[u];
         }
     } else {
-        const Vec<T, N> v = load_vec<T, N>(static_cast<const T*>(p) + c);
-#pragma unroll
-        for (int u = 0; u < N; ++u) out[u] = to_f32(v.v[u]);
+        Vec<T, N> v;
+        v.load(static_cast<const T*>(p) + c);
+        v.get(out);
     }
 }
 
@@ -96,12 +199,13 @@ struct NormGradParams {
     int cols, w_f32;
 };
 
-// CTAs of the backward pass that own partial column sums: four on each of
-// 152 SMs.
-constexpr int kNormMaxPartials = 608;
+constexpr int kSms = 152;  // streaming multiprocessors of a GB300
 
-cudaError_t launch_norm(const NormParams& p, int dtype, bool vec, cudaStream_t st);
-cudaError_t launch_norm_grad(const NormGradParams& p, int dtype, bool vec, cudaStream_t st);
+// CTAs of the backward pass that own partial column sums.
+constexpr int kNormMaxPartials = 4 * kSms;
+
+cudaError_t launch_norm(const NormParams& p, int dtype, int lie, cudaStream_t st);
+cudaError_t launch_norm_grad(const NormGradParams& p, int dtype, int lie, cudaStream_t st);
 
 // ------------------------------------------------------------ tokens <-> rows
 struct TokenParams {
@@ -114,9 +218,9 @@ struct TokenParams {
     int T, kp, H;
 };
 
-cudaError_t launch_permute(const TokenParams& p, int dtype, bool vec, cudaStream_t st, bool pdl);
-cudaError_t launch_unpermute(const TokenParams& p, int dtype, bool vec, cudaStream_t st);
-cudaError_t launch_unpermute_grad(const TokenParams& p, int dtype, bool vec, cudaStream_t st);
+cudaError_t launch_permute(const TokenParams& p, int dtype, int lie, cudaStream_t st);
+cudaError_t launch_unpermute(const TokenParams& p, int dtype, int lie, cudaStream_t st);
+cudaError_t launch_unpermute_grad(const TokenParams& p, int dtype, int lie, cudaStream_t st);
 
 // ------------------------------------------------------------ routing gradient
 struct RouteGradParams {

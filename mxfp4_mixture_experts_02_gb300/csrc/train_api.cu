@@ -24,8 +24,10 @@ bool all_on(uintptr_t a, P... p) {
     return (on(p, a) && ...);
 }
 
-// Rows move in 16-byte accesses when every row starts on such a boundary.
-bool wide_rows(int64_t cols, int bytes) { return cols * bytes % 16 == 0; }
+// on_grid: every tensor of rows starts on a 16-byte boundary.
+int lie_of(bool on_grid, int64_t cols, int bytes) {
+    return !on_grid ? kSingle : cols * bytes % 16 == 0 ? kGrid : kOff;
+}
 
 int check_norm(const moe_norm_shape* s) {
     if (!s) return MOE_ERR_NULL;
@@ -120,8 +122,8 @@ int moe_layer_norm(const moe_norm_shape* s, const void* x, const void* residual,
     if (!all_on(b, x, residual, h, y) || !all_on(wb, weight, bias) || !all_on(4, mean, rstd)) return MOE_ERR_ALIGN;
     NormParams p{x, residual, weight, bias, residual ? h : nullptr, y, mean, rstd, s->rows, s->cols,
                  s->w_dtype == MOE_DTYPE_F32, s->eps};
-    const bool vec = wide_rows(s->cols, b) && all_on(16, x, residual, p.h, y, weight, bias);
-    return rc_of(launch_norm(p, s->dtype, vec, cu(stream)));
+    const bool on_grid = all_on(16, x, residual, p.h, y, weight, bias);
+    return rc_of(launch_norm(p, s->dtype, lie_of(on_grid, s->cols, b), cu(stream)));
 }
 
 int moe_layer_norm_backward(const moe_norm_shape* s, const void* dy, const void* h, const float* mean,
@@ -140,8 +142,8 @@ int moe_layer_norm_backward(const moe_norm_shape* s, const void* dy, const void*
     if (s->rows == 0 && !sums) return MOE_OK;
     NormGradParams p{dy, h, weight, dh, mean, rstd, dx, dweight, dbias, sums ? static_cast<float*>(ws) : nullptr,
                      s->rows, s->cols, s->w_dtype == MOE_DTYPE_F32};
-    const bool vec = wide_rows(s->cols, b) && all_on(16, dy, h, weight, dh, dx);
-    return rc_of(launch_norm_grad(p, s->dtype, vec, cu(stream)));
+    const bool on_grid = all_on(16, dy, h, weight, dh, dx);
+    return rc_of(launch_norm_grad(p, s->dtype, lie_of(on_grid, s->cols, b), cu(stream)));
 }
 
 int moe_token_map_workspace_bytes(const moe_token_shape* s, size_t* bytes) {
@@ -193,8 +195,8 @@ int moe_permute(const moe_token_shape* s, const void* x, const int32_t* c_map, v
     if (!x || !c_map || !rows) return MOE_ERR_NULL;
     const int b = elem_bytes(s->dtype);
     if (!all_on(b, x, rows) || !on(c_map, 4)) return MOE_ERR_ALIGN;
-    const bool vec = wide_rows(s->hidden, b) && all_on(16, x, rows);
-    return rc_of(launch_permute(token_params(*s, x, c_map, nullptr, rows), s->dtype, vec, cu(stream), false));
+    const int lie = lie_of(all_on(16, x, rows), s->hidden, b);
+    return rc_of(launch_permute(token_params(*s, x, c_map, nullptr, rows), s->dtype, lie, cu(stream)));
 }
 
 int moe_permute_backward(const moe_token_shape* s, const void* drows, const int32_t* c_map, void* dx,
@@ -205,8 +207,8 @@ int moe_permute_backward(const moe_token_shape* s, const void* drows, const int3
     if (!drows || !c_map || !dx) return MOE_ERR_NULL;
     const int b = elem_bytes(s->dtype);
     if (!all_on(b, drows, dx) || !on(c_map, 4)) return MOE_ERR_ALIGN;
-    const bool vec = wide_rows(s->hidden, b) && all_on(16, drows, dx);
-    return rc_of(launch_unpermute(token_params(*s, drows, c_map, nullptr, dx), s->dtype, vec, cu(stream)));
+    const int lie = lie_of(all_on(16, drows, dx), s->hidden, b);
+    return rc_of(launch_unpermute(token_params(*s, drows, c_map, nullptr, dx), s->dtype, lie, cu(stream)));
 }
 
 int moe_unpermute(const moe_token_shape* s, const void* rows, const float* topk_w, const int32_t* c_map, void* out,
@@ -217,8 +219,8 @@ int moe_unpermute(const moe_token_shape* s, const void* rows, const float* topk_
     if (!rows || !topk_w || !c_map || !out) return MOE_ERR_NULL;
     const int b = elem_bytes(s->dtype);
     if (!all_on(b, rows, out) || !all_on(4, topk_w, c_map)) return MOE_ERR_ALIGN;
-    const bool vec = wide_rows(s->hidden, b) && all_on(16, rows, out);
-    return rc_of(launch_unpermute(token_params(*s, rows, c_map, topk_w, out), s->dtype, vec, cu(stream)));
+    const int lie = lie_of(all_on(16, rows, out), s->hidden, b);
+    return rc_of(launch_unpermute(token_params(*s, rows, c_map, topk_w, out), s->dtype, lie, cu(stream)));
 }
 
 int moe_unpermute_backward(const moe_token_shape* s, const void* dout, const void* rows, const float* topk_w,
@@ -229,11 +231,11 @@ int moe_unpermute_backward(const moe_token_shape* s, const void* dout, const voi
     if (!dout || !rows || !topk_w || !c_map || !drows || !dtopk_w) return MOE_ERR_NULL;
     const int b = elem_bytes(s->dtype);
     if (!all_on(b, dout, rows, drows) || !all_on(4, topk_w, c_map, dtopk_w)) return MOE_ERR_ALIGN;
-    const bool vec = wide_rows(s->hidden, b) && all_on(16, dout, rows, drows);
+    const int lie = lie_of(all_on(16, dout, rows, drows), s->hidden, b);
     TokenParams p = token_params(*s, rows, c_map, topk_w, drows);
     p.dout = dout;
     p.dw = dtopk_w;
-    return rc_of(launch_unpermute_grad(p, s->dtype, vec, cu(stream)));
+    return rc_of(launch_unpermute_grad(p, s->dtype, lie, cu(stream)));
 }
 
 int moe_route_backward(const moe_token_shape* s, const uint16_t* shared_logit, float shared_scale, const int32_t* ids,
