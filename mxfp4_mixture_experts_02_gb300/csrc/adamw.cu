@@ -2,8 +2,8 @@
 //   g' = g c                      (c: an optional scale on the device)
 //   m  = m + (1 - b1) (g' - m),   v = v + (1 - b2) (g'^2 - v)
 //   p  = p (1 - lr wd) - lr / (1 - b1^t) m / (sqrt(v) / sqrt(1 - b2^t) + eps)
-// Every operation is rounded by itself (no contraction), so the 8-bit codes
-// follow from the formulas alone.
+// m and v are rounded operation by operation, as the formulas are written, so
+// the states follow from them alone.
 //
 // 8-bit states: m and sqrt(v) as E4M3 codes with one power-of-two scale per
 // 32 values, 2^e with e = floor(log2 max) - 7 (the largest magnitude lies in
@@ -21,6 +21,7 @@ namespace {
 
 constexpr int kAdamwThreads = 256;
 constexpr int kE = 8;  // elements per thread: four threads share a block of 32
+constexpr uint64_t kGamma = 0x9E3779B97F4A7C15ull;
 
 // SplitMix64's output function at state z.
 __device__ __forceinline__ uint64_t mix64(uint64_t z) {
@@ -29,203 +30,275 @@ __device__ __forceinline__ uint64_t mix64(uint64_t z) {
     return z ^ (z >> 31);
 }
 
-// x (|x| < 256) to an E4M3 code with 16 random bits: the 20 mantissa bits
-// below E4M3's three are compared with the random bits by an add and cut off.
-// Below 2^-6 E4M3's steps stop shrinking at 2^-9; moved up by 2^-6 a value's
-// own steps have that size.
-__device__ __forceinline__ float e4m3_random(float x, uint32_t r16) {
-    float a = fabsf(x);
-    if (!(a <= 3.0e38f)) return __uint_as_float(0x7FC00000u);  // no E4M3 infinity: stored as NaN
-    const float lift = a < 0.015625f ? 0.015625f : 0.f;
-    a = __fadd_rn(a, lift);
-    a = __uint_as_float((__float_as_uint(a) + (r16 << 4)) & ~0xFFFFFu);
-    return copysignf(__fsub_rn(a, lift), x);
+__device__ __forceinline__ float2 pair(const float (&v)[kE], int k) { return make_float2(v[2 * k], v[2 * k + 1]); }
+__device__ __forceinline__ void put_pair(float (&v)[kE], int k, float2 a) {
+    v[2 * k] = a.x;
+    v[2 * k + 1] = a.y;
 }
 
-__device__ __forceinline__ float e4m3_to_f32(uint32_t c) {
-    const float v = e4m3_pos_to_float(c & 127u);
-    return (c & 128u) ? -v : v;
-}
+// a - b, rounded once
+__device__ __forceinline__ float2 sub2(float2 a, float2 b) { return fma2(b, both(-1.f), a); }
 
-// The scale exponent of a block with largest magnitude amax.
-__device__ __forceinline__ int state_exponent(float amax) {
-    const int e = mx_shared_exponent(amax, 7);
-    return e < -126 ? -126 : (e > 126 ? 126 : e);
-}
-
-template <typename G>
-__device__ __forceinline__ void load8(float (&g)[kE], const G* p) {
+// Eight E4M3 codes times 2^(scale code - 127).
+__device__ __forceinline__ void decode8(float (&f)[kE], uint2 c, uint32_t scale) {
+    const float s = __uint_as_float(scale << 23);
 #pragma unroll
-    for (int i = 0; i < kE; i += kFull<G>) {
-        Vec<G, kFull<G>> v;
-        float f[kFull<G>];
-        v.load(p + i);
-        v.get(f);
-#pragma unroll
-        for (int u = 0; u < kFull<G>; ++u) g[i + u] = f[u];
+    for (int k = 0; k < kE / 2; ++k) {
+        const uint32_t two = (k < 2 ? c.x : c.y) >> (16 * (k & 1));
+        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two & 0xFFFFu), __NV_E4M3);
+        put_pair(f, k, mul2(__half22float2(__half2(h)), both(s)));
     }
 }
 
-template <typename G, bool MX>
-__global__ void __launch_bounds__(kAdamwThreads) adamw_kernel(const __grid_constant__ AdamwBatch<kAdamwMaxTensors> b) {
-    __shared__ int s_tensor;
+// The exponent of a block's scale from the bits of its largest magnitude, and
+// for the roots from those of the largest square: floor(log2 sqrt(v)) is half
+// of floor(log2 v), rounded down.
+__device__ __forceinline__ int exponent_of(uint32_t amax) { return max(static_cast<int>(amax >> 23) - 134, -126); }
+__device__ __forceinline__ int root_exponent_of(uint32_t vmax) {
+    if (vmax == 0) return -126;
+    const int e = vmax < 0x00800000u ? -118 - __clz(vmax) : static_cast<int>(vmax >> 23) - 127;
+    return (e >> 1) - 7;
+}
+
+// The codes of eight values, rounded at random.  Divided by 2^120 an E4M3
+// number becomes the fp32 number whose exponent and three leading mantissa bits
+// are its code, below 2^-6 too, where both stop normalising: so the random
+// bits are added to the 20 bits that are cut off.  x = value / scale, at most
+// 256 (and a rounding) in magnitude; r: the random bits, `high` half of each.
+template <bool SIGNED, bool HIGH>
+__device__ __forceinline__ uint2 encode8(const float (&v)[kE], float inv, const uint32_t (&r)[kE]) {
+    uint32_t q[kE];
+#pragma unroll
+    for (int k = 0; k < kE / 2; ++k) {
+        const float2 y = mul2(mul2(pair(v, k), both(inv)), both(__uint_as_float(7u << 23)));
+        const uint32_t r0 = HIGH ? r[2 * k] >> 16 : r[2 * k] & 0xFFFFu;
+        const uint32_t r1 = HIGH ? r[2 * k + 1] >> 16 : r[2 * k + 1] & 0xFFFFu;
+        q[2 * k] = __float_as_uint(y.x) + (r0 << 4);
+        q[2 * k + 1] = __float_as_uint(y.y) + (r1 << 4);
+        if (!SIGNED) {  // what is not zero keeps the smallest code
+            q[2 * k] = max(q[2 * k], min(__float_as_uint(v[2 * k]), 1u << 20));
+            q[2 * k + 1] = max(q[2 * k + 1], min(__float_as_uint(v[2 * k + 1]), 1u << 20));
+        }
+    }
+    uint32_t w[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const uint32_t* a = q + 4 * h;
+        // bits 27 .. 20 (27 is zero) to the top byte, four together
+        w[h] = __byte_perm(__byte_perm(a[0] << 4, a[1] << 4, 0x0073), __byte_perm(a[2] << 4, a[3] << 4, 0x0073), 0x5410);
+        if (SIGNED)
+            w[h] |= __byte_perm(__byte_perm(a[0], a[1], 0x0073), __byte_perm(a[2], a[3], 0x0073), 0x5410) & 0x80808080u;
+    }
+    return make_uint2(w[0], w[1]);
+}
+
+// Takes out what is not finite: those of the eight become zero, and NaN codes
+// in the answer, to be put over the codes.
+__device__ __forceinline__ uint2 take_out_nan(float (&v)[kE]) {
+    uint2 nan = make_uint2(0u, 0u);
+#pragma unroll
+    for (int u = 0; u < kE; ++u)
+        if (!(fabsf(v[u]) <= 3.4e38f)) {
+            (u < 4 ? nan.x : nan.y) |= 0x7Fu << (8 * (u & 3));
+            v[u] = 0.f;
+        }
+    return nan;
+}
+
+// The largest bits of the block's magnitudes, over the four threads that hold
+// it.  Bits of magnitudes order as these do, with NaN on top.
+__device__ __forceinline__ uint32_t block_max(const float (&v)[kE], uint32_t lanes) {
+    uint32_t a = 0u;
+#pragma unroll
+    for (int u = 0; u < kE; ++u) a = max(a, __float_as_uint(fabsf(v[u])));
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) a = max(a, __shfl_xor_sync(lanes, a, o));
+    return a;
+}
+
+// Eight consecutive elements in accesses of 32 bytes (neighbouring threads then
+// fill whole lines) or, from a 16-byte boundary, of 16.
+__device__ __forceinline__ void load8(float (&g)[kE], const float* p, bool by32) {
+    if (by32) {
+        ptx::ld_global_32(g, p);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < kE; i += 4) {
+        Vec<float, 4> v;
+        float f[4];
+        v.load(p + i);
+        v.get(f);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) g[i + u] = f[u];
+    }
+}
+__device__ __forceinline__ void load8(float (&g)[kE], const __nv_bfloat16* p, bool) {
+    Vec<__nv_bfloat16, 8> v;
+    v.load(p);
+    v.get(g);
+}
+
+// Elements i .. i + live - 1 one by one, zeros behind them.
+template <typename G>
+__device__ __forceinline__ void load_some(float (&g)[kE], const G* p, int live) {
+#pragma unroll
+    for (int u = 0; u < kE; ++u) g[u] = u < live ? to_f32(p[u]) : 0.f;
+}
+
+__device__ __forceinline__ void store8(float* p, const float (&v)[kE], bool by32) {
+    if (by32) {
+        ptx::st_global_32(p, v);
+        return;
+    }
+#pragma unroll
+    for (int u = 0; u < kE; u += 4)
+        *reinterpret_cast<float4*>(p + u) = make_float4(v[u], v[u + 1], v[u + 2], v[u + 3]);
+}
+
+__device__ __forceinline__ void store_some(float* p, const float (&v)[kE], int live) {
+#pragma unroll
+    for (int u = 0; u < kE; ++u)
+        if (u < live) p[u] = v[u];
+}
+
+__device__ __forceinline__ uint2 load_codes(const uint8_t* p, int live, bool wide) {
+    if (wide) return *reinterpret_cast<const uint2*>(p);
+    uint2 c = make_uint2(0u, 0u);
+#pragma unroll
+    for (int u = 0; u < kE; ++u)
+        if (u < live) (u < 4 ? c.x : c.y) |= static_cast<uint32_t>(p[u]) << (8 * (u & 3));
+    return c;
+}
+
+__device__ __forceinline__ void store_codes(uint8_t* p, uint2 c, int live, bool wide) {
+    if (wide) {
+        *reinterpret_cast<uint2*>(p) = c;
+        return;
+    }
+#pragma unroll
+    for (int u = 0; u < kE; ++u)
+        if (u < live) p[u] = static_cast<uint8_t>((u < 4 ? c.x : c.y) >> (8 * (u & 3)));
+}
+
+template <typename G, bool MX, int N>
+__global__ void __launch_bounds__(kAdamwThreads, 4) adamw_kernel(const __grid_constant__ AdamwBatch<N> b) {
     float clip = 1.f;
     if (b.grad_scale) {
         clip = *b.grad_scale;
         if (!isfinite(clip)) return;  // a gradient that overflowed: the step is skipped
     }
-    for (uint32_t item = blockIdx.x; item < b.items; item += gridDim.x) {
-        if (threadIdx.x == 0) {  // the last tensor that starts at or before the item
-            int lo = 0, hi = b.count - 1;
-            while (lo < hi) {
-                const int mid = (lo + hi + 1) >> 1;
-                if (b.t[mid].first_item <= item) lo = mid;
-                else hi = mid - 1;
-            }
-            s_tensor = lo;
-        }
-        __syncthreads();
-        const AdamwTensor& t = b.t[s_tensor];
-        const int64_t begin = static_cast<int64_t>(item - t.first_item) * kAdamwItem;
-        const int64_t end = min(begin + kAdamwItem, t.n);
-        const G* gp = static_cast<const G*>(t.g);
-        for (int64_t i0 = begin; i0 < end; i0 += kAdamwThreads * kE) {
-            const int64_t i = i0 + threadIdx.x * kE;
-            const int live = i < end ? static_cast<int>(min(static_cast<int64_t>(kE), end - i)) : 0;
-            const bool wide = t.vec && live == kE;
+    // the CTA's items lie one behind the other; the first one's tensor is the
+    // last that starts at or before it
+    const uint32_t per = (b.items + gridDim.x - 1) / gridDim.x;
+    const uint32_t first = blockIdx.x * per, last = min(first + per, b.items);
+    int at = 0;
+    for (int lo = 0, hi = b.count - 1; lo < hi; at = lo) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (b.t[mid].first_item <= first) lo = mid;
+        else hi = mid - 1;
+    }
+    for (uint32_t item = first; item < last; ++item) {
+        while (at + 1 < b.count && b.t[at + 1].first_item <= item) ++at;
+        const AdamwTensor& t = b.t[at];
+        {
+            const int64_t i = static_cast<int64_t>(item - t.first_item) * kAdamwItem + threadIdx.x * kE;
+            const int live = static_cast<int>(max(int64_t(0), min(static_cast<int64_t>(kE), t.n - i)));
+            const bool wide = t.vec && live == kE, by32 = t.vec == 2;
+            const G* gp = static_cast<const G*>(t.g) + i;
+            float *fm = static_cast<float*>(t.m) + i, *fv = static_cast<float*>(t.v) + i;
+            uint8_t *cm = static_cast<uint8_t*>(t.m) + i, *cv = static_cast<uint8_t*>(t.v) + i;
             float p[kE], g[kE], m[kE], v[kE];
             if (wide) {
-                load8(p, t.p + i);
-                load8(g, gp + i);
+                load8(p, t.p + i, by32);
+                load8(g, gp, by32);
             } else {
-#pragma unroll
-                for (int u = 0; u < kE; ++u) {
-                    p[u] = u < live ? t.p[i + u] : 0.f;
-                    g[u] = u < live ? to_f32(gp[i + u]) : 0.f;
-                }
+                load_some(p, t.p + i, live);
+                load_some(g, gp, live);
             }
             if (MX) {
-                const uint8_t* mc = static_cast<const uint8_t*>(t.m);
-                const uint8_t* vc = static_cast<const uint8_t*>(t.v);
-                float sm = 0.f, sv = 0.f;
-                if (live) {
-                    sm = exp2_int(t.ms[i >> 5] - 127);
-                    sv = exp2_int(t.vs[i >> 5] - 127);
-                }
-                if (wide) {
-                    const uint2 cm = *reinterpret_cast<const uint2*>(mc + i), cv = *reinterpret_cast<const uint2*>(vc + i);
+                const uint32_t sm = live ? t.ms[i >> 5] : 0u, sv = live ? t.vs[i >> 5] : 0u;
+                decode8(m, load_codes(cm, live, wide), sm);
+                decode8(v, load_codes(cv, live, wide), sv);
 #pragma unroll
-                    for (int u = 0; u < kE; ++u) {
-                        m[u] = __fmul_rn(e4m3_to_f32(((u < 4 ? cm.x : cm.y) >> (8 * (u & 3))) & 255u), sm);
-                        v[u] = __fmul_rn(e4m3_to_f32(((u < 4 ? cv.x : cv.y) >> (8 * (u & 3))) & 255u), sv);
-                    }
-                } else {
-#pragma unroll
-                    for (int u = 0; u < kE; ++u) {
-                        m[u] = u < live ? __fmul_rn(e4m3_to_f32(mc[i + u]), sm) : 0.f;
-                        v[u] = u < live ? __fmul_rn(e4m3_to_f32(vc[i + u]), sv) : 0.f;
-                    }
-                }
-#pragma unroll
-                for (int u = 0; u < kE; ++u) v[u] = __fmul_rn(v[u], v[u]);
+                for (int k = 0; k < kE / 2; ++k) put_pair(v, k, mul2(pair(v, k), pair(v, k)));
             } else if (wide) {
-                load8(m, static_cast<const float*>(t.m) + i);
-                load8(v, static_cast<const float*>(t.v) + i);
+                load8(m, fm, by32);
+                load8(v, fv, by32);
             } else {
-#pragma unroll
-                for (int u = 0; u < kE; ++u) {
-                    m[u] = u < live ? static_cast<const float*>(t.m)[i + u] : 0.f;
-                    v[u] = u < live ? static_cast<const float*>(t.v)[i + u] : 0.f;
-                }
+                load_some(m, fm, live);
+                load_some(v, fv, live);
             }
             float root[kE];
 #pragma unroll
-            for (int u = 0; u < kE; ++u) {
-                const float gc = b.grad_scale ? __fmul_rn(g[u], clip) : g[u];
-                m[u] = __fadd_rn(m[u], __fmul_rn(__fsub_rn(gc, m[u]), b.one_minus_beta1));
-                v[u] = __fadd_rn(v[u], __fmul_rn(__fsub_rn(__fmul_rn(gc, gc), v[u]), b.one_minus_beta2));
-                root[u] = __fsqrt_rn(v[u]);
-                const float den = __fadd_rn(__fmul_rn(root[u], b.inv_root_bc2), b.eps);
-                p[u] = __fsub_rn(__fmul_rn(p[u], b.decay), __fmul_rn(__fdiv_rn(m[u], den), b.step_size));
+            for (int k = 0; k < kE / 2; ++k) {
+                const float2 g2 = b.grad_scale ? mul2(pair(g, k), both(clip)) : pair(g, k);
+                const float2 m2 = add2(pair(m, k), mul2(sub2(g2, pair(m, k)), both(b.one_minus_beta1)));
+                const float2 v2 = add2(pair(v, k), mul2(sub2(mul2(g2, g2), pair(v, k)), both(b.one_minus_beta2)));
+                // the root and the quotient to within two units in the last
+                // place: p moves by lr of it
+                const float2 r2 = make_float2(ptx::sqrt_approx(v2.x), ptx::sqrt_approx(v2.y));
+                const float2 den = fma2(r2, both(b.inv_root_bc2), both(b.eps));
+                const float2 q = make_float2(__fdividef(m2.x, den.x), __fdividef(m2.y, den.y));
+                put_pair(m, k, m2);
+                put_pair(v, k, v2);
+                put_pair(root, k, r2);
+                put_pair(p, k, fma2(q, both(-b.step_size), mul2(pair(p, k), both(b.decay))));
             }
-            if (wide) {
-#pragma unroll
-                for (int u = 0; u < kE; u += 4)
-                    *reinterpret_cast<float4*>(t.p + i + u) = make_float4(p[u], p[u + 1], p[u + 2], p[u + 3]);
-            } else {
-#pragma unroll
-                for (int u = 0; u < kE; ++u)
-                    if (u < live) t.p[i + u] = p[u];
-            }
+            if (wide) store8(t.p + i, p, by32);
+            else store_some(t.p + i, p, live);
             if (MX) {
-                float am = 0.f, av = 0.f;
-#pragma unroll
-                for (int u = 0; u < kE; ++u)
-                    if (u < live) am = fmaxf(am, fabsf(m[u])), av = fmaxf(av, root[u]);
-#pragma unroll
-                for (int o = 1; o < 4; o <<= 1) {
-                    am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
-                    av = fmaxf(av, __shfl_xor_sync(0xffffffffu, av, o));
+                uint32_t am = block_max(m, 0xffffffffu), av = block_max(v, 0xffffffffu);
+                uint2 m_nan = make_uint2(0u, 0u), v_nan = m_nan;
+                if (max(am, av) >= 0x7F800000u) {  // the same for the block's threads
+                    const uint32_t four = 0xFu << (threadIdx.x & 28);
+                    m_nan = take_out_nan(m);
+                    v_nan = take_out_nan(v);
+                    take_out_nan(root);
+                    am = block_max(m, four);
+                    av = block_max(v, four);
                 }
-                const int em = state_exponent(am), ev = state_exponent(av);
-                const float im = exp2_int(-em), iv = exp2_int(-ev);
-                uint32_t cm[kE], cv[kE];
+                // elements 2k and 2k + 1 take the halves of number k + 1
+                uint32_t r[kE];
+                uint64_t z = b.seed + ((static_cast<uint64_t>(t.counter + i) >> 1) + 1) * kGamma;
 #pragma unroll
-                for (int u = 0; u < kE; u += 2) {
-                    // elements 2k and 2k + 1 take the halves of number k + 1
-                    const uint64_t k1 = (static_cast<uint64_t>(t.counter + i + u) >> 1) + 1;
-                    const uint64_t r = mix64(b.seed + k1 * 0x9E3779B97F4A7C15ull);
-#pragma unroll
-                    for (int w = 0; w < 2; ++w) {
-                        const uint32_t bits = static_cast<uint32_t>(r >> (32 * w));
-                        const float qm = e4m3_random(__fmul_rn(m[u + w], im), bits & 0xFFFFu);
-                        float qv = e4m3_random(__fmul_rn(root[u + w], iv), bits >> 16);
-                        if (root[u + w] != 0.f && qv < 0.001953125f) qv = 0.001953125f;  // a NaN stays one
-                        const uint32_t c = e4m3x2(qm, qv);
-                        cm[u + w] = c & 255u;
-                        cv[u + w] = c >> 8;
-                    }
+                for (int u = 0; u < kE; u += 2, z += kGamma) {
+                    const uint64_t x = mix64(z);
+                    r[u] = static_cast<uint32_t>(x);
+                    r[u + 1] = static_cast<uint32_t>(x >> 32);
                 }
-                uint8_t* mo = static_cast<uint8_t*>(t.m);
-                uint8_t* vo = static_cast<uint8_t*>(t.v);
-                if (wide) {
-                    *reinterpret_cast<uint2*>(mo + i) = make_uint2(cm[0] | cm[1] << 8 | cm[2] << 16 | cm[3] << 24,
-                                                                   cm[4] | cm[5] << 8 | cm[6] << 16 | cm[7] << 24);
-                    *reinterpret_cast<uint2*>(vo + i) = make_uint2(cv[0] | cv[1] << 8 | cv[2] << 16 | cv[3] << 24,
-                                                                   cv[4] | cv[5] << 8 | cv[6] << 16 | cv[7] << 24);
-                } else {
-#pragma unroll
-                    for (int u = 0; u < kE; ++u)
-                        if (u < live) mo[i + u] = static_cast<uint8_t>(cm[u]), vo[i + u] = static_cast<uint8_t>(cv[u]);
-                }
+                const int em = exponent_of(am), ev = root_exponent_of(av);
+                uint2 c = encode8<true, false>(m, __uint_as_float(static_cast<uint32_t>(127 - em) << 23), r);
+                uint2 d = encode8<false, true>(root, __uint_as_float(static_cast<uint32_t>(127 - ev) << 23), r);
+                c.x |= m_nan.x, c.y |= m_nan.y, d.x |= v_nan.x, d.y |= v_nan.y;
+                store_codes(cm, c, live, wide);
+                store_codes(cv, d, live, wide);
                 if (live && (i & 31) == 0) {
                     t.ms[i >> 5] = static_cast<uint8_t>(em + 127);
                     t.vs[i >> 5] = static_cast<uint8_t>(ev + 127);
                 }
             } else if (wide) {
-                float *mo = static_cast<float*>(t.m) + i, *vo = static_cast<float*>(t.v) + i;
-#pragma unroll
-                for (int u = 0; u < kE; u += 4) {
-                    *reinterpret_cast<float4*>(mo + u) = make_float4(m[u], m[u + 1], m[u + 2], m[u + 3]);
-                    *reinterpret_cast<float4*>(vo + u) = make_float4(v[u], v[u + 1], v[u + 2], v[u + 3]);
-                }
+                store8(fm, m, by32);
+                store8(fv, v, by32);
             } else {
-#pragma unroll
-                for (int u = 0; u < kE; ++u)
-                    if (u < live) static_cast<float*>(t.m)[i + u] = m[u], static_cast<float*>(t.v)[i + u] = v[u];
+                store_some(fm, m, live);
+                store_some(fv, v, live);
             }
         }
-        __syncthreads();  // s_tensor is read until here
     }
 }
 
 }  // namespace
 
-cudaError_t launch_adamw(const AdamwBatch<kAdamwMaxTensors>& b, int g_dtype, bool mx, cudaStream_t st) {
-    const dim3 grid(b.items < kSms * 8u ? b.items : kSms * 8u);
+template <int N>
+cudaError_t launch_adamw(const AdamwBatch<N>& b, int g_dtype, bool mx, cudaStream_t st) {
+    const dim3 grid(b.items < kSms * 4u ? b.items : kSms * 4u);
     auto go = [&](auto kernel) { return launch_kernel(kernel, grid, dim3(kAdamwThreads), 0, st, false, b); };
-    if (g_dtype == MOE_DTYPE_F32) return mx ? go(adamw_kernel<float, true>) : go(adamw_kernel<float, false>);
-    return mx ? go(adamw_kernel<__nv_bfloat16, true>) : go(adamw_kernel<__nv_bfloat16, false>);
+    if (g_dtype == MOE_DTYPE_F32) return mx ? go(adamw_kernel<float, true, N>) : go(adamw_kernel<float, false, N>);
+    return mx ? go(adamw_kernel<__nv_bfloat16, true, N>) : go(adamw_kernel<__nv_bfloat16, false, N>);
 }
+
+template cudaError_t launch_adamw<kAdamwFew>(const AdamwBatch<kAdamwFew>&, int, bool, cudaStream_t);
+template cudaError_t launch_adamw<kAdamwMany>(const AdamwBatch<kAdamwMany>&, int, bool, cudaStream_t);
 
 }  // namespace moe

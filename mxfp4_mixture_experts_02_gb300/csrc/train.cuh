@@ -245,26 +245,28 @@ struct AdamwTensor {
     int64_t n;
     int64_t counter;
     uint32_t first_item;
-    uint32_t vec;  // every pointer is aligned for wide accesses
+    uint32_t vec;  // 1: every pointer is aligned for 16-byte accesses, 2: and for 32-byte ones; else 0
 };
 
-// A launch's tensors travel in its parameters (at most 32764 bytes).
-constexpr int kAdamwMaxTensors = 448;
+// A launch's tensors travel in its parameters (at most 32764 bytes): the usual
+// few, or as many as fit.
+constexpr int kAdamwFew = 32, kAdamwMany = 448;
 
 template <int N>
 struct AdamwBatch {
     AdamwTensor t[N];
     const float* grad_scale;
     uint64_t seed;
-    float beta1, one_minus_beta1, beta2, one_minus_beta2, decay, step_size, inv_root_bc2, eps;
+    float one_minus_beta1, one_minus_beta2, decay, step_size, inv_root_bc2, eps;
     uint32_t items;
     int count;
 };
 
-static_assert(sizeof(AdamwBatch<kAdamwMaxTensors>) <= 32764, "kernel parameters");
+static_assert(sizeof(AdamwBatch<kAdamwMany>) <= 32764, "kernel parameters");
 
-constexpr int64_t kAdamwItem = 4096;  // elements of one work item
+constexpr int64_t kAdamwItem = 2048;  // elements of one work item: eight for each thread of a CTA
 
-cudaError_t launch_adamw(const AdamwBatch<kAdamwMaxTensors>& b, int g_dtype, bool mx, cudaStream_t st);
+template <int N>
+cudaError_t launch_adamw(const AdamwBatch<N>& b, int g_dtype, bool mx, cudaStream_t st);
 
 }  // namespace moe

@@ -98,6 +98,42 @@ TokenParams token_params(const moe_token_shape& s, const void* src, const int32_
     return p;
 }
 
+// One launch over the next tensors from number i on (at most N); advances i and
+// the random sequence's element counter.
+template <int N>
+int step_some(const moe_adamw_tensor* tensors, int32_t count, int32_t& i, const moe_adamw_config& c,
+              const float* grad_scale, int64_t& counter, cudaStream_t st) {
+    // up to 32 KB: not on the stack of a caller's thread
+    std::unique_ptr<AdamwBatch<N>> b(new (std::nothrow) AdamwBatch<N>());
+    if (!b) return MOE_ERR_CUDA;
+    b->grad_scale = grad_scale;
+    b->seed = c.seed;
+    b->one_minus_beta1 = static_cast<float>(1.0 - c.beta1);
+    b->one_minus_beta2 = static_cast<float>(1.0 - c.beta2);
+    b->decay = static_cast<float>(1.0 - c.lr * c.weight_decay);
+    b->step_size = static_cast<float>(c.lr / (1.0 - std::pow(c.beta1, static_cast<double>(c.step))));
+    b->inv_root_bc2 = static_cast<float>(1.0 / std::sqrt(1.0 - std::pow(c.beta2, static_cast<double>(c.step))));
+    b->eps = static_cast<float>(c.eps);
+    const bool mx = c.state == MOE_STATE_MXFP8;
+    int64_t items = 0;
+    for (; i < count && b->count < N; ++i) {
+        const moe_adamw_tensor& t = tensors[i];
+        if (t.n == 0) continue;
+        const int64_t mine = (t.n + kAdamwItem - 1) / kAdamwItem;
+        if (items + mine > 0xFFFFFFFFll) break;
+        AdamwTensor& k = b->t[b->count++];
+        k = AdamwTensor{t.p, t.g, t.m, t.v, t.m_scale, t.v_scale, t.n, counter, static_cast<uint32_t>(items), 0};
+        const auto wide = [&](uintptr_t a) {  // bf16 gradients take 16 bytes, codes 8
+            return on(t.p, a) && on(t.g, c.g_dtype == MOE_DTYPE_F32 ? a : 16) && (mx ? all_on(8, t.m, t.v) : all_on(a, t.m, t.v));
+        };
+        k.vec = wide(32) ? 2 : wide(16) ? 1 : 0;
+        counter += (t.n + 31) & ~int64_t(31);
+        items += mine;
+    }
+    b->items = static_cast<uint32_t>(items);
+    return items ? rc_of(launch_adamw(*b, c.g_dtype, mx, st)) : MOE_OK;
+}
+
 }  // namespace
 }  // namespace moe
 
@@ -272,43 +308,15 @@ int moe_adamw(const moe_adamw_tensor* tensors, int32_t count, const moe_adamw_co
         if (!on(t.p, 4) || !on(t.g, gb) || (!mx && !all_on(4, t.m, t.v))) return MOE_ERR_ALIGN;
     }
     if (!on(grad_scale, 4)) return MOE_ERR_ALIGN;
-    // the parameters of a launch: 32 KB, so not on the stack of a caller's thread
-    std::unique_ptr<AdamwBatch<kAdamwMaxTensors>> b(new (std::nothrow) AdamwBatch<kAdamwMaxTensors>());
-    if (!b) return MOE_ERR_CUDA;
-    b->grad_scale = grad_scale;
-    b->seed = c->seed;
-    b->beta1 = static_cast<float>(c->beta1);
-    b->one_minus_beta1 = static_cast<float>(1.0 - c->beta1);
-    b->beta2 = static_cast<float>(c->beta2);
-    b->one_minus_beta2 = static_cast<float>(1.0 - c->beta2);
-    b->decay = static_cast<float>(1.0 - c->lr * c->weight_decay);
-    b->step_size = static_cast<float>(c->lr / (1.0 - std::pow(c->beta1, static_cast<double>(c->step))));
-    b->inv_root_bc2 = static_cast<float>(1.0 / std::sqrt(1.0 - std::pow(c->beta2, static_cast<double>(c->step))));
-    b->eps = static_cast<float>(c->eps);
-    int64_t counter = 0, items = 0;
-    auto flush = [&]() -> int {
-        if (!b->count) return MOE_OK;
-        b->items = static_cast<uint32_t>(items);
-        const int r = rc_of(launch_adamw(*b, c->g_dtype, mx, cu(stream)));
-        b->count = 0;
-        items = 0;
-        return r;
-    };
-    for (int32_t i = 0; i < count; ++i) {
-        const moe_adamw_tensor& t = tensors[i];
-        if (t.n == 0) continue;
-        const int64_t mine = (t.n + kAdamwItem - 1) / kAdamwItem;
-        if (b->count == kAdamwMaxTensors || items + mine > 0xFFFFFFFFll) {
-            const int rc = flush();
-            if (rc) return rc;
-        }
-        AdamwTensor& k = b->t[b->count++];
-        k = AdamwTensor{t.p, t.g, t.m, t.v, t.m_scale, t.v_scale, t.n, counter, static_cast<uint32_t>(items), 0};
-        k.vec = on(t.p, 16) && on(t.g, 16) && (mx ? all_on(8, t.m, t.v) : all_on(16, t.m, t.v));
-        counter += (t.n + 31) & ~int64_t(31);
-        items += mine;
+    int64_t counter = 0;
+    for (int32_t i = 0; i < count;) {
+        // up to kAdamwMany tensors a launch
+        const int rc = count - i <= kAdamwFew
+                           ? step_some<kAdamwFew>(tensors, count, i, *c, grad_scale, counter, cu(stream))
+                           : step_some<kAdamwMany>(tensors, count, i, *c, grad_scale, counter, cu(stream));
+        if (rc) return rc;
     }
-    return flush();
+    return MOE_OK;
 }
 
 }  // extern "C"
