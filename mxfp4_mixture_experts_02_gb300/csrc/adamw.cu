@@ -21,6 +21,9 @@ namespace {
 
 constexpr int kAdamwThreads = 256;
 constexpr int kE = 8;  // elements per thread: four threads share a block of 32
+// Resident CTAs: as many as hold two steps' reads in registers.
+template <bool MX>
+constexpr uint32_t kAdamwCtas = MX ? 3 : 2;
 constexpr uint64_t kGamma = 0x9E3779B97F4A7C15ull;
 
 // SplitMix64's output function at state z.
@@ -60,36 +63,48 @@ __device__ __forceinline__ int root_exponent_of(uint32_t vmax) {
     return (e >> 1) - 7;
 }
 
-// The codes of eight values, rounded at random.  Divided by 2^120 an E4M3
-// number becomes the fp32 number whose exponent and three leading mantissa bits
-// are its code, below 2^-6 too, where both stop normalising: so the random
-// bits are added to the 20 bits that are cut off.  x = value / scale, at most
-// 256 (and a rounding) in magnitude; r: the random bits, `high` half of each.
-template <bool SIGNED, bool HIGH>
-__device__ __forceinline__ uint2 encode8(const float (&v)[kE], float inv, const uint32_t (&r)[kE]) {
-    uint32_t q[kE];
+// x / 2^120 for x = value / scale, |x| <= 256 and a rounding: an fp32 number
+// whose exponent and three leading mantissa bits are x's E4M3 code, below 2^-6
+// too, where both stop normalising.  So rounding at random is adding random
+// bits to the 20 bits below, which are then cut off.
+__device__ __forceinline__ float2 to_code(float2 v, float inv) {
+    return mul2(mul2(v, both(inv)), both(__uint_as_float(7u << 23)));
+}
+
+// The codes of two such numbers (bits 27 .. 20; bit 27 is zero) in the low
+// bytes, and their signs.
+__device__ __forceinline__ uint32_t two_codes(uint32_t a, uint32_t b) { return __byte_perm(a << 4, b << 4, 0x0073); }
+__device__ __forceinline__ uint32_t two_signs(uint32_t a, uint32_t b) { return __byte_perm(a, b, 0x0073) & 0x8080u; }
+
+// Codes of m and of the roots, from the random sequence's state z for the first
+// two elements: elements c and c + 1 take the halves of one 64-bit number, m
+// the low 16 bits of a half and the root the high ones.
+__device__ __forceinline__ void encode8(uint2& c, uint2& d, const float (&m)[kE], float inv_m, const float (&root)[kE],
+                                        float inv_r, uint64_t z) {
+    uint32_t cm[kE / 2], cr[kE / 2];
 #pragma unroll
-    for (int k = 0; k < kE / 2; ++k) {
-        const float2 y = mul2(mul2(pair(v, k), both(inv)), both(__uint_as_float(7u << 23)));
-        const uint32_t r0 = HIGH ? r[2 * k] >> 16 : r[2 * k] & 0xFFFFu;
-        const uint32_t r1 = HIGH ? r[2 * k + 1] >> 16 : r[2 * k + 1] & 0xFFFFu;
-        q[2 * k] = __float_as_uint(y.x) + (r0 << 4);
-        q[2 * k + 1] = __float_as_uint(y.y) + (r1 << 4);
-        if (!SIGNED) {  // what is not zero keeps the smallest code
-            q[2 * k] = max(q[2 * k], min(__float_as_uint(v[2 * k]), 1u << 20));
-            q[2 * k + 1] = max(q[2 * k + 1], min(__float_as_uint(v[2 * k + 1]), 1u << 20));
+    for (int k = 0; k < kE / 2; ++k, z += kGamma) {
+        const uint64_t x = mix64(z);
+        const uint32_t r0 = static_cast<uint32_t>(x), r1 = static_cast<uint32_t>(x >> 32);
+        const float2 ym = to_code(pair(m, k), inv_m), yr = to_code(pair(root, k), inv_r);
+        const uint32_t m0 = __float_as_uint(ym.x) + ((r0 & 0xFFFFu) << 4);
+        const uint32_t m1 = __float_as_uint(ym.y) + ((r1 & 0xFFFFu) << 4);
+        const uint32_t q0 = __float_as_uint(yr.x) + ((r0 >> 16) << 4), q1 = __float_as_uint(yr.y) + ((r1 >> 16) << 4);
+        cm[k] = two_codes(m0, m1) | two_signs(m0, m1);
+        cr[k] = two_codes(q0, q1);
+    }
+    c = make_uint2(__byte_perm(cm[0], cm[1], 0x5410), __byte_perm(cm[2], cm[3], 0x5410));
+    d = make_uint2(__byte_perm(cr[0], cr[1], 0x5410), __byte_perm(cr[2], cr[3], 0x5410));
+    // a root that is not zero keeps the smallest code; seldom is one so far
+    // below the block's largest
+    const auto zero_byte = [](uint32_t w) { return (w - 0x01010101u) & ~w & 0x80808080u; };
+    if (zero_byte(d.x) | zero_byte(d.y)) {
+#pragma unroll
+        for (int u = 0; u < kE; ++u) {
+            uint32_t& w = u < 4 ? d.x : d.y;
+            if (root[u] != 0.f && ((w >> (8 * (u & 3))) & 255u) == 0u) w |= 1u << (8 * (u & 3));
         }
     }
-    uint32_t w[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const uint32_t* a = q + 4 * h;
-        // bits 27 .. 20 (27 is zero) to the top byte, four together
-        w[h] = __byte_perm(__byte_perm(a[0] << 4, a[1] << 4, 0x0073), __byte_perm(a[2] << 4, a[3] << 4, 0x0073), 0x5410);
-        if (SIGNED)
-            w[h] |= __byte_perm(__byte_perm(a[0], a[1], 0x0073), __byte_perm(a[2], a[3], 0x0073), 0x5410) & 0x80808080u;
-    }
-    return make_uint2(w[0], w[1]);
 }
 
 // Takes out what is not finite: those of the eight become zero, and NaN codes
@@ -105,14 +120,14 @@ __device__ __forceinline__ uint2 take_out_nan(float (&v)[kE]) {
     return nan;
 }
 
-// The largest bits of the block's magnitudes, over the four threads that hold
-// it.  Bits of magnitudes order as these do, with NaN on top.
-__device__ __forceinline__ uint32_t block_max(const float (&v)[kE], uint32_t lanes) {
-    uint32_t a = 0u;
+// The largest magnitude of the block, over the four threads that hold it; what
+// is NaN does not count.
+__device__ __forceinline__ float block_max(const float (&v)[kE]) {
+    float a = 0.f;
 #pragma unroll
-    for (int u = 0; u < kE; ++u) a = max(a, __float_as_uint(fabsf(v[u])));
+    for (int u = 0; u < kE; ++u) a = fmaxf(a, fabsf(v[u]));
 #pragma unroll
-    for (int o = 1; o < 4; o <<= 1) a = max(a, __shfl_xor_sync(lanes, a, o));
+    for (int o = 1; o < 4; o <<= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
     return a;
 }
 
@@ -133,18 +148,37 @@ __device__ __forceinline__ void load8(float (&g)[kE], const float* p, bool by32)
         for (int u = 0; u < 4; ++u) g[i + u] = f[u];
     }
 }
-__device__ __forceinline__ void load8(float (&g)[kE], const __nv_bfloat16* p, bool) {
-    Vec<__nv_bfloat16, 8> v;
-    v.load(p);
-    v.get(g);
-}
-
 // Elements i .. i + live - 1 one by one, zeros behind them.
 template <typename G>
 __device__ __forceinline__ void load_some(float (&g)[kE], const G* p, int live) {
 #pragma unroll
     for (int u = 0; u < kE; ++u) g[u] = u < live ? to_f32(p[u]) : 0.f;
 }
+
+// Eight gradients as they were read.
+template <typename G>
+struct Grad8;
+template <>
+struct Grad8<float> {
+    float f[kE];
+    __device__ __forceinline__ void load(const float* p, bool by32) { load8(f, p, by32); }
+    __device__ __forceinline__ void load_some(const float* p, int live) { moe::load_some(f, p, live); }
+    __device__ __forceinline__ void get(float (&g)[kE]) const {
+#pragma unroll
+        for (int u = 0; u < kE; ++u) g[u] = f[u];
+    }
+};
+template <>
+struct Grad8<__nv_bfloat16> {
+    Vec<__nv_bfloat16, 8> v;
+    __device__ __forceinline__ void load(const __nv_bfloat16* p, bool) { v.w = ptx::ld_global_16(p); }
+    __device__ __forceinline__ void load_some(const __nv_bfloat16* p, int live) {
+        float f[kE];
+        moe::load_some(f, p, live);
+        v.set(f);
+    }
+    __device__ __forceinline__ void get(float (&g)[kE]) const { v.get(g); }
+};
 
 __device__ __forceinline__ void store8(float* p, const float (&v)[kE], bool by32) {
     if (by32) {
@@ -162,8 +196,7 @@ __device__ __forceinline__ void store_some(float* p, const float (&v)[kE], int l
         if (u < live) p[u] = v[u];
 }
 
-__device__ __forceinline__ uint2 load_codes(const uint8_t* p, int live, bool wide) {
-    if (wide) return *reinterpret_cast<const uint2*>(p);
+__device__ __forceinline__ uint2 load_codes(const uint8_t* p, int live) {
     uint2 c = make_uint2(0u, 0u);
 #pragma unroll
     for (int u = 0; u < kE; ++u)
@@ -171,119 +204,192 @@ __device__ __forceinline__ uint2 load_codes(const uint8_t* p, int live, bool wid
     return c;
 }
 
-__device__ __forceinline__ void store_codes(uint8_t* p, uint2 c, int live, bool wide) {
-    if (wide) {
-        *reinterpret_cast<uint2*>(p) = c;
-        return;
-    }
+__device__ __forceinline__ void store_codes(uint8_t* p, uint2 c, int live) {
 #pragma unroll
     for (int u = 0; u < kE; ++u)
         if (u < live) p[u] = static_cast<uint8_t>((u < 4 ? c.x : c.y) >> (8 * (u & 3)));
 }
 
+// A tensor's elements from a work item's first on.
+template <typename G>
+struct ItemPtrs {
+    float* p;
+    const G* g;
+    void *m, *v;
+    uint8_t *ms, *vs;
+    uint64_t z;  // the random sequence's state for the item's first two elements
+};
+
+// What a thread reads for one step: kE elements, with MXFP8 states as codes and
+// their scales.
+template <typename G, bool MX>
+struct Step {
+    float p[kE];
+    Grad8<G> g;
+    float m[MX ? 1 : kE], v[MX ? 1 : kE];
+    uint2 cm, cv;
+    uint32_t sm, sv;
+};
+
+// The reads of a step, all on their way before the first is used (inline
+// assembly keeps them there).  FULL: all elements are in the tensor and in wide
+// accesses; else `live` are.
+template <bool FULL, typename G, bool MX>
+__device__ __forceinline__ void fetch(Step<G, MX>& s, const ItemPtrs<G>& t, uint32_t o, int live, bool by32) {
+    const uint8_t *cm = static_cast<const uint8_t*>(t.m) + o, *cv = static_cast<const uint8_t*>(t.v) + o;
+    const float *fm = static_cast<const float*>(t.m) + o, *fv = static_cast<const float*>(t.v) + o;
+    if constexpr (FULL) {
+        load8(s.p, t.p + o, by32);
+        s.g.load(t.g + o, by32);
+    } else {
+        load_some(s.p, t.p + o, live);
+        s.g.load_some(t.g + o, live);
+    }
+    if constexpr (MX) {
+        s.sm = s.sv = 0u;
+        if (FULL || live > 0) {
+            s.sm = ptx::ld_global_u8(t.ms + o / 32);
+            s.sv = ptx::ld_global_u8(t.vs + o / 32);
+        }
+        s.cm = FULL ? ptx::ld_global_8(cm) : load_codes(cm, live);
+        s.cv = FULL ? ptx::ld_global_8(cv) : load_codes(cv, live);
+    } else if constexpr (FULL) {
+        load8(s.m, fm, by32);
+        load8(s.v, fv, by32);
+    } else {
+        load_some(s.m, fm, live);
+        load_some(s.v, fv, live);
+    }
+}
+
+// The update of a step's elements, and their writes.
+template <bool FULL, typename G, bool MX, typename B>
+__device__ __forceinline__ void update(const Step<G, MX>& s, const B& b, const ItemPtrs<G>& t, uint32_t o, int live,
+                                       bool by32, float clip) {
+    float p[kE], g[kE], m[kE], v[kE], root[kE];
+    s.g.get(g);
+    if constexpr (MX) {
+        decode8(m, s.cm, s.sm);
+        decode8(v, s.cv, s.sv);
+#pragma unroll
+        for (int k = 0; k < kE / 2; ++k) put_pair(v, k, mul2(pair(v, k), pair(v, k)));
+    } else {
+#pragma unroll
+        for (int u = 0; u < kE; ++u) m[u] = s.m[u], v[u] = s.v[u];
+    }
+#pragma unroll
+    for (int k = 0; k < kE / 2; ++k) {
+        const float2 g2 = b.grad_scale ? mul2(pair(g, k), both(clip)) : pair(g, k);
+        const float2 m2 = add2(pair(m, k), mul2(sub2(g2, pair(m, k)), both(b.one_minus_beta1)));
+        const float2 v2 = add2(pair(v, k), mul2(sub2(mul2(g2, g2), pair(v, k)), both(b.one_minus_beta2)));
+        // root and quotient by the hardware's approximations, within 2^-21 of
+        // the update: p itself is rounded to 2^-24 of its larger size
+        const float2 r2 = make_float2(ptx::sqrt_approx(v2.x), ptx::sqrt_approx(v2.y));
+        const float2 den = fma2(r2, both(b.inv_root_bc2), both(b.eps));
+        const float2 q = mul2(m2, make_float2(ptx::rcp_approx(den.x), ptx::rcp_approx(den.y)));
+        put_pair(m, k, m2);
+        put_pair(v, k, v2);
+        put_pair(root, k, r2);
+        put_pair(p, k, fma2(q, both(-b.step_size), mul2(pair(s.p, k), both(b.decay))));
+    }
+    uint8_t *cm = static_cast<uint8_t*>(t.m) + o, *cv = static_cast<uint8_t*>(t.v) + o;
+    float *fm = static_cast<float*>(t.m) + o, *fv = static_cast<float*>(t.v) + o;
+    if (FULL) store8(t.p + o, p, by32);
+    else store_some(t.p + o, p, live);
+    if constexpr (!MX) {
+        if (FULL) {
+            store8(fm, m, by32);
+            store8(fv, v, by32);
+        } else {
+            store_some(fm, m, live);
+            store_some(fv, v, live);
+        }
+        return;
+    }
+    float am = block_max(m);
+    int ev = root_exponent_of(__float_as_uint(block_max(v)));
+    // zero, or NaN where something is not finite
+    float2 odd = both(0.f);
+#pragma unroll
+    for (int k = 0; k < kE / 2; ++k) odd = fma2(pair(v, k), both(0.f), fma2(pair(m, k), both(0.f), odd));
+    const uint32_t finite = __ballot_sync(0xffffffffu, odd.x + odd.y == 0.f);
+    uint2 m_nan = make_uint2(0u, 0u), r_nan = m_nan;
+    if (finite != 0xffffffffu) {  // the scales of such blocks are those of the rest
+        m_nan = take_out_nan(m);
+        r_nan = take_out_nan(root);
+        am = block_max(m);
+        const float ar = block_max(root);
+        if (((finite >> (threadIdx.x & 28)) & 15u) != 15u) ev = exponent_of(__float_as_uint(ar));
+    }
+    const int em = exponent_of(__float_as_uint(am));
+    uint2 c, d;
+    encode8(c, d, m, __uint_as_float(static_cast<uint32_t>(127 - em) << 23), root,
+            __uint_as_float(static_cast<uint32_t>(127 - ev) << 23), t.z + static_cast<uint64_t>(o / 2) * kGamma);
+    c.x |= m_nan.x, c.y |= m_nan.y, d.x |= r_nan.x, d.y |= r_nan.y;
+    if (FULL) {
+        *reinterpret_cast<uint2*>(cm) = c;
+        *reinterpret_cast<uint2*>(cv) = d;
+    } else {
+        store_codes(cm, c, live);
+        store_codes(cv, d, live);
+    }
+    if ((FULL || live > 0) && (threadIdx.x & 3) == 0) {
+        t.ms[o / 32] = static_cast<uint8_t>(em + 127);
+        t.vs[o / 32] = static_cast<uint8_t>(ev + 127);
+    }
+}
+
 template <typename G, bool MX, int N>
-__global__ void __launch_bounds__(kAdamwThreads, 4) adamw_kernel(const __grid_constant__ AdamwBatch<N> b) {
+__global__ void __launch_bounds__(kAdamwThreads, kAdamwCtas<MX>) adamw_kernel(const __grid_constant__ AdamwBatch<N> b) {
     float clip = 1.f;
     if (b.grad_scale) {
         clip = *b.grad_scale;
         if (!isfinite(clip)) return;  // a gradient that overflowed: the step is skipped
     }
-    // the CTA's items lie one behind the other; the first one's tensor is the
-    // last that starts at or before it
-    const uint32_t per = (b.items + gridDim.x - 1) / gridDim.x;
-    const uint32_t first = blockIdx.x * per, last = min(first + per, b.items);
     int at = 0;
-    for (int lo = 0, hi = b.count - 1; lo < hi; at = lo) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (b.t[mid].first_item <= first) lo = mid;
-        else hi = mid - 1;
-    }
-    for (uint32_t item = first; item < last; ++item) {
-        while (at + 1 < b.count && b.t[at + 1].first_item <= item) ++at;
+    for (uint32_t item = blockIdx.x; item < b.items; item += gridDim.x) {
+        // an item's tensor is the last that starts at or before it
+        for (int lo = at, hi = b.count - 1; lo < hi; at = lo) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (b.t[mid].first_item <= item) lo = mid;
+            else hi = mid - 1;
+        }
         const AdamwTensor& t = b.t[at];
-        {
-            const int64_t i = static_cast<int64_t>(item - t.first_item) * kAdamwItem + threadIdx.x * kE;
-            const int live = static_cast<int>(max(int64_t(0), min(static_cast<int64_t>(kE), t.n - i)));
-            const bool wide = t.vec && live == kE, by32 = t.vec == 2;
-            const G* gp = static_cast<const G*>(t.g) + i;
-            float *fm = static_cast<float*>(t.m) + i, *fv = static_cast<float*>(t.v) + i;
-            uint8_t *cm = static_cast<uint8_t*>(t.m) + i, *cv = static_cast<uint8_t*>(t.v) + i;
-            float p[kE], g[kE], m[kE], v[kE];
-            if (wide) {
-                load8(p, t.p + i, by32);
-                load8(g, gp, by32);
-            } else {
-                load_some(p, t.p + i, live);
-                load_some(g, gp, live);
-            }
-            if (MX) {
-                const uint32_t sm = live ? t.ms[i >> 5] : 0u, sv = live ? t.vs[i >> 5] : 0u;
-                decode8(m, load_codes(cm, live, wide), sm);
-                decode8(v, load_codes(cv, live, wide), sv);
-#pragma unroll
-                for (int k = 0; k < kE / 2; ++k) put_pair(v, k, mul2(pair(v, k), pair(v, k)));
-            } else if (wide) {
-                load8(m, fm, by32);
-                load8(v, fv, by32);
-            } else {
-                load_some(m, fm, live);
-                load_some(v, fv, live);
-            }
-            float root[kE];
-#pragma unroll
-            for (int k = 0; k < kE / 2; ++k) {
-                const float2 g2 = b.grad_scale ? mul2(pair(g, k), both(clip)) : pair(g, k);
-                const float2 m2 = add2(pair(m, k), mul2(sub2(g2, pair(m, k)), both(b.one_minus_beta1)));
-                const float2 v2 = add2(pair(v, k), mul2(sub2(mul2(g2, g2), pair(v, k)), both(b.one_minus_beta2)));
-                // the root and the quotient to within two units in the last
-                // place: p moves by lr of it
-                const float2 r2 = make_float2(ptx::sqrt_approx(v2.x), ptx::sqrt_approx(v2.y));
-                const float2 den = fma2(r2, both(b.inv_root_bc2), both(b.eps));
-                const float2 q = make_float2(__fdividef(m2.x, den.x), __fdividef(m2.y, den.y));
-                put_pair(m, k, m2);
-                put_pair(v, k, v2);
-                put_pair(root, k, r2);
-                put_pair(p, k, fma2(q, both(-b.step_size), mul2(pair(p, k), both(b.decay))));
-            }
-            if (wide) store8(t.p + i, p, by32);
-            else store_some(t.p + i, p, live);
-            if (MX) {
-                uint32_t am = block_max(m, 0xffffffffu), av = block_max(v, 0xffffffffu);
-                uint2 m_nan = make_uint2(0u, 0u), v_nan = m_nan;
-                if (max(am, av) >= 0x7F800000u) {  // the same for the block's threads
-                    const uint32_t four = 0xFu << (threadIdx.x & 28);
-                    m_nan = take_out_nan(m);
-                    v_nan = take_out_nan(v);
-                    take_out_nan(root);
-                    am = block_max(m, four);
-                    av = block_max(v, four);
+        const int64_t begin = static_cast<int64_t>(item - t.first_item) * b.item_elems;
+        const int size = static_cast<int>(min(static_cast<int64_t>(b.item_elems), t.n - begin));
+        ItemPtrs<G> q;
+        q.p = t.p + begin;
+        q.g = static_cast<const G*>(t.g) + begin;
+        q.m = static_cast<uint8_t*>(t.m) + begin * (MX ? 1 : 4);
+        q.v = static_cast<uint8_t*>(t.v) + begin * (MX ? 1 : 4);
+        q.ms = t.ms + begin / 32;
+        q.vs = t.vs + begin / 32;
+        // elements c and c + 1 (c even) take number c / 2 + 1 of the sequence
+        q.z = b.seed + ((static_cast<uint64_t>(t.counter + begin) >> 1) + 1) * kGamma;
+        const bool by32 = t.vec == 2;
+        int done = 0;
+        const uint32_t mine = threadIdx.x * kE;
+        if (t.vec && size >= kAdamwStep) {
+            // the next step's reads are on their way during one
+            Step<G, MX> s0, s1;
+            const int full = size / kAdamwStep * kAdamwStep;
+            fetch<true>(s0, q, mine, kE, by32);
+            for (; done < full; done += 2 * kAdamwStep) {
+                const uint32_t o0 = done + mine, o1 = o0 + kAdamwStep, o2 = o1 + kAdamwStep;
+                if (done + kAdamwStep < full) fetch<true>(s1, q, o1, kE, by32);
+                update<true>(s0, b, q, o0, kE, by32, clip);
+                if (done + kAdamwStep < full) {
+                    if (done + 2 * kAdamwStep < full) fetch<true>(s0, q, o2, kE, by32);
+                    update<true>(s1, b, q, o1, kE, by32, clip);
                 }
-                // elements 2k and 2k + 1 take the halves of number k + 1
-                uint32_t r[kE];
-                uint64_t z = b.seed + ((static_cast<uint64_t>(t.counter + i) >> 1) + 1) * kGamma;
-#pragma unroll
-                for (int u = 0; u < kE; u += 2, z += kGamma) {
-                    const uint64_t x = mix64(z);
-                    r[u] = static_cast<uint32_t>(x);
-                    r[u + 1] = static_cast<uint32_t>(x >> 32);
-                }
-                const int em = exponent_of(am), ev = root_exponent_of(av);
-                uint2 c = encode8<true, false>(m, __uint_as_float(static_cast<uint32_t>(127 - em) << 23), r);
-                uint2 d = encode8<false, true>(root, __uint_as_float(static_cast<uint32_t>(127 - ev) << 23), r);
-                c.x |= m_nan.x, c.y |= m_nan.y, d.x |= v_nan.x, d.y |= v_nan.y;
-                store_codes(cm, c, live, wide);
-                store_codes(cv, d, live, wide);
-                if (live && (i & 31) == 0) {
-                    t.ms[i >> 5] = static_cast<uint8_t>(em + 127);
-                    t.vs[i >> 5] = static_cast<uint8_t>(ev + 127);
-                }
-            } else if (wide) {
-                store8(fm, m, by32);
-                store8(fv, v, by32);
-            } else {
-                store_some(fm, m, live);
-                store_some(fv, v, live);
             }
+            done = full;
+        }
+        for (; done < size; done += kAdamwStep) {
+            const int o = done + static_cast<int>(mine), live = max(0, min(size - o, kE));
+            Step<G, MX> s;
+            fetch<false>(s, q, o, live, false);
+            update<false>(s, b, q, o, live, false, clip);
         }
     }
 }
@@ -292,7 +398,8 @@ __global__ void __launch_bounds__(kAdamwThreads, 4) adamw_kernel(const __grid_co
 
 template <int N>
 cudaError_t launch_adamw(const AdamwBatch<N>& b, int g_dtype, bool mx, cudaStream_t st) {
-    const dim3 grid(b.items < kSms * 4u ? b.items : kSms * 4u);
+    const uint32_t most = kSms * (mx ? kAdamwCtas<true> : kAdamwCtas<false>);
+    const dim3 grid(b.items < most ? b.items : most);
     auto go = [&](auto kernel) { return launch_kernel(kernel, grid, dim3(kAdamwThreads), 0, st, false, b); };
     if (g_dtype == MOE_DTYPE_F32) return mx ? go(adamw_kernel<float, true, N>) : go(adamw_kernel<float, false, N>);
     return mx ? go(adamw_kernel<__nv_bfloat16, true, N>) : go(adamw_kernel<__nv_bfloat16, false, N>);

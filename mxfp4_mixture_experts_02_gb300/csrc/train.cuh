@@ -259,12 +259,13 @@ struct AdamwBatch {
     uint64_t seed;
     float one_minus_beta1, one_minus_beta2, decay, step_size, inv_root_bc2, eps;
     uint32_t items;
+    int item_elems;  // of a work item: a multiple of kAdamwStep
     int count;
 };
 
 static_assert(sizeof(AdamwBatch<kAdamwMany>) <= 32764, "kernel parameters");
 
-constexpr int64_t kAdamwItem = 2048;  // elements of one work item: eight for each thread of a CTA
+constexpr int kAdamwStep = 2048;  // elements that a CTA takes at once: eight for each thread
 
 template <int N>
 cudaError_t launch_adamw(const AdamwBatch<N>& b, int g_dtype, bool mx, cudaStream_t st);

@@ -1,5 +1,6 @@
 // C entries of the training operators around the experts (declared in
 // include/moe_api.h): argument checks on the host, then the launches.
+#include <algorithm>
 #include <cmath>
 #include <memory>
 #include <new>
@@ -115,11 +116,15 @@ int step_some(const moe_adamw_tensor* tensors, int32_t count, int32_t& i, const 
     b->inv_root_bc2 = static_cast<float>(1.0 / std::sqrt(1.0 - std::pow(c.beta2, static_cast<double>(c.step))));
     b->eps = static_cast<float>(c.eps);
     const bool mx = c.state == MOE_STATE_MXFP8;
+    // items of up to eight steps, eight items for each of four CTAs on an SM
+    int64_t total = 0;
+    for (int32_t j = i, taken = 0; j < count && taken < N; ++j) taken += tensors[j].n > 0, total += tensors[j].n;
+    b->item_elems = kAdamwStep * static_cast<int>(std::clamp<int64_t>(total / (int64_t(kAdamwStep) * kSms * 32), 1, 8));
     int64_t items = 0;
     for (; i < count && b->count < N; ++i) {
         const moe_adamw_tensor& t = tensors[i];
         if (t.n == 0) continue;
-        const int64_t mine = (t.n + kAdamwItem - 1) / kAdamwItem;
+        const int64_t mine = (t.n + b->item_elems - 1) / b->item_elems;
         if (items + mine > 0xFFFFFFFFll) break;
         AdamwTensor& k = b->t[b->count++];
         k = AdamwTensor{t.p, t.g, t.m, t.v, t.m_scale, t.v_scale, t.n, counter, static_cast<uint32_t>(items), 0};
