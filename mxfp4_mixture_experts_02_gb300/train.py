@@ -59,32 +59,55 @@ SIGS = {
 }
 
 
+_fns = {}
+
+
 def _call(name, *args):
-    from . import _call as call
+    f = _fns.get(name)
+    if f is None:
+        from . import lib
 
-    return call(name, *args)
+        f = _fns[name] = getattr(lib(), name)
+    rc = f(*args)
+    if rc:
+        from . import MoeError
+
+        raise MoeError(name, rc)
 
 
-def _stream(t):
-    return torch.cuda.current_stream(t.device).cuda_stream
+# The current stream's handle of a device (by index), without the Stream object
+# that torch.cuda.current_stream builds: 2 us of a 10 us call.
+_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _check(name, t, dtype=None, shape=None, device=None):
-    """A contiguous CUDA tensor of the given type, shape and device; None passes."""
-    if t is None:
-        return
-    if not t.is_cuda or not t.is_contiguous():
+def _index(name, t):
+    """Device index of a contiguous CUDA tensor, the first of a call's."""
+    i = t.get_device()
+    if i < 0 or not t.is_contiguous():
         raise ValueError("%s: expected a contiguous CUDA tensor" % name)
-    if dtype is not None and t.dtype != dtype:
+    return i
+
+
+def _check(name, t, dtype, shape, index):
+    """A contiguous tensor of the given type, shape and device index; None passes."""
+    if t is None or (t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous()):
+        return
+    if t.get_device() < 0 or not t.is_contiguous():
+        raise ValueError("%s: expected a contiguous CUDA tensor" % name)
+    if t.dtype is not dtype:
         raise ValueError("%s: expected %s, got %s" % (name, dtype, t.dtype))
-    if shape is not None and t.shape != shape:
+    if t.shape != shape:
         raise ValueError("%s: expected shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
-    if device is not None and t.device != device:
-        raise ValueError("%s: expected a tensor on %s, got %s" % (name, device, t.device))
+    raise ValueError("%s: expected a tensor on device %d, got %s" % (name, index, t.device))
+
+
+def _check_ws(ws, index):
+    if ws is not None:
+        _check("ws", ws, torch.uint8, ws.shape, index)
 
 
 def _rows_dtype(name, t):
@@ -95,44 +118,51 @@ def _rows_dtype(name, t):
 
 
 # ------------------------------------------------------------------ layer norm
-def _norm_args(x, weight, bias, eps):
+def _norm_args(name, x, weight, bias, eps):
+    """(C shape, rows, device index) of a norm over the last dimension of x."""
+    index = _index(name, x)
     if x.dim() < 1 or x.shape[-1] < 1:
-        raise ValueError("layer norm: expected rows of at least one column")
+        raise ValueError("%s: expected rows of at least one column" % name)
     cols = x.shape[-1]
     rows = x.numel() // cols
-    dtype = w_dtype = _rows_dtype("x", x)
-    for n, t in (("weight", weight), ("bias", bias)):
-        if t is not None:
-            if t.dtype != x.dtype and t.dtype != torch.float32:
-                raise ValueError("%s: expected float32 or the rows' type, got %s" % (n, t.dtype))
-            _check(n, t, None, (cols,), x.device)
-            w_dtype = _DTYPES[t.dtype]
-    if weight is not None and bias is not None and weight.dtype != bias.dtype:
-        raise ValueError("weight and bias: expected one type, got %s and %s" % (weight.dtype, bias.dtype))
-    return _NormShape(rows, cols, dtype, w_dtype, eps), rows, cols
+    dtype = _rows_dtype(name, x)
+    p = bias if weight is None else weight
+    w_dtype = dtype
+    if p is not None:
+        if p.dtype is not x.dtype and p.dtype is not torch.float32:
+            raise ValueError("weight and bias: expected float32 or the rows' type, got %s" % p.dtype)
+        _check("weight", weight, p.dtype, (cols,), index)
+        _check("bias", bias, p.dtype, (cols,), index)
+        w_dtype = _DTYPES[p.dtype]
+    return _NormShape(rows, cols, dtype, w_dtype, eps), rows, index
 
 
 def moe_layer_norm(x, weight=None, bias=None, residual=None, eps=1e-5, y=None, h=None, mean=None, rstd=None):
     """Layer norm of h = x + residual over the last dimension: (y, h, mean, rstd),
     with mean and rstd fp32 [rows] for the backward pass.  Without a residual h is x."""
-    _check("x", x)
-    s, rows, _ = _norm_args(x, weight, bias, eps)
-    for n, t in (("residual", residual), ("y", y), ("h", h)):
-        _check(n, t, x.dtype, x.shape, x.device)
-    for n, t in (("mean", mean), ("rstd", rstd)):
-        _check(n, t, torch.float32, (rows,), x.device)
+    s, rows, index = _norm_args("x", x, weight, bias, eps)
+    dtype, shape = x.dtype, x.shape
+    _check("residual", residual, dtype, shape, index)
     if y is None:
         y = torch.empty_like(x)
+    else:
+        _check("y", y, dtype, shape, index)
     if residual is None:
         h = x
     elif h is None:
         h = torch.empty_like(x)
+    else:
+        _check("h", h, dtype, shape, index)
     if mean is None:
         mean = torch.empty(rows, dtype=torch.float32, device=x.device)
+    else:
+        _check("mean", mean, torch.float32, (rows,), index)
     if rstd is None:
         rstd = torch.empty(rows, dtype=torch.float32, device=x.device)
+    else:
+        _check("rstd", rstd, torch.float32, (rows,), index)
     _call("moe_layer_norm", ctypes.byref(s), x.data_ptr(), _ptr(residual), _ptr(weight), _ptr(bias),
-          h.data_ptr(), y.data_ptr(), mean.data_ptr(), rstd.data_ptr(), _stream(x))
+          h.data_ptr(), y.data_ptr(), mean.data_ptr(), rstd.data_ptr(), _stream(index))
     return y, h, mean, rstd
 
 
@@ -151,15 +181,16 @@ def moe_layer_norm_backward(dy, h, mean, rstd, weight=None, dh=None, bias_grad=T
                             dbias=None, ws=None):
     """(dx, dweight, dbias) of moe_layer_norm.  dh: the gradient that reaches h beside the norm, added to dx.
     dweight (fp32) is None without a weight, dbias (fp32) without bias_grad."""
-    _check("h", h)
-    s, rows, cols = _norm_args(h, weight, None, 0.0)
-    for n, t in (("dy", dy), ("dh", dh), ("dx", dx)):
-        _check(n, t, h.dtype, h.shape, h.device)
-    for n, t in (("mean", mean), ("rstd", rstd)):
-        _check(n, t, torch.float32, (rows,), h.device)
-    for n, t in (("dweight", dweight), ("dbias", dbias)):
-        _check(n, t, torch.float32, (cols,), h.device)
-    _check("ws", ws, torch.uint8, None, h.device)
+    s, rows, index = _norm_args("h", h, weight, None, 0.0)
+    dtype, shape, cols = h.dtype, h.shape, h.shape[-1]
+    _check("dy", dy, dtype, shape, index)
+    _check("dh", dh, dtype, shape, index)
+    _check("mean", mean, torch.float32, (rows,), index)
+    _check("rstd", rstd, torch.float32, (rows,), index)
+    _check("dx", dx, dtype, shape, index)
+    _check("dweight", dweight, torch.float32, (cols,), index)
+    _check("dbias", dbias, torch.float32, (cols,), index)
+    _check_ws(ws, index)
     if dx is None:
         dx = torch.empty_like(h)
     if weight is None:
@@ -174,7 +205,7 @@ def moe_layer_norm_backward(dy, h, mean, rstd, weight=None, dh=None, bias_grad=T
         ws = layer_norm_workspace(rows, cols, h.device)
     _call("moe_layer_norm_backward", ctypes.byref(s), dy.data_ptr(), h.data_ptr(), mean.data_ptr(), rstd.data_ptr(),
           _ptr(weight), _ptr(dh), dx.data_ptr(), _ptr(dweight), _ptr(dbias), _ptr(ws),
-          0 if ws is None else ws.numel(), _stream(h))
+          0 if ws is None else ws.numel(), _stream(index))
     return dx, dweight, dbias
 
 
@@ -222,81 +253,86 @@ def token_map_workspace(shape: MoeTokenShape, device="cuda") -> torch.Tensor:
 
 def moe_token_map(shape: MoeTokenShape, topk_ids, ws=None, maps: MoeTokenMap = None) -> MoeTokenMap:
     """Sorts the slots of topk_ids int32 [T, k'] by expert (the maps of moe_sort, in buffers of their own)."""
-    dev, kp, n = topk_ids.device, shape.kp, shape.T * shape.kp
-    _check("topk_ids", topk_ids, torch.int32, (shape.T, kp))
-    Et = shape.E_local + shape.num_shared
+    kp, n, Et = shape.kp, shape.T * shape.kp, shape.E_local + shape.num_shared
+    index = _index("topk_ids", topk_ids)
+    _check("topk_ids", topk_ids, torch.int32, (shape.T, kp), index)
     if maps is None:
+        dev = topk_ids.device
         maps = MoeTokenMap(torch.empty(n, dtype=torch.int32, device=dev),
                            torch.empty((shape.T, kp), dtype=torch.int32, device=dev),
                            torch.empty(Et + 1, dtype=torch.int32, device=dev))
     else:
-        _check("a_map", maps.a_map, torch.int32, (n,), dev)
-        _check("c_map", maps.c_map, torch.int32, (shape.T, kp), dev)
-        _check("expert_offsets", maps.expert_offsets, torch.int32, (Et + 1,), dev)
-    _check("ws", ws, torch.uint8, None, dev)
+        _check("a_map", maps.a_map, torch.int32, (n,), index)
+        _check("c_map", maps.c_map, torch.int32, (shape.T, kp), index)
+        _check("expert_offsets", maps.expert_offsets, torch.int32, (Et + 1,), index)
     if ws is None:
-        ws = token_map_workspace(shape, dev)
+        ws = token_map_workspace(shape, topk_ids.device)
+    else:
+        _check_ws(ws, index)
     s = shape.c()
     _call("moe_token_map", ctypes.byref(s), topk_ids.data_ptr(), maps.a_map.data_ptr(), maps.c_map.data_ptr(),
-          maps.expert_offsets.data_ptr(), ws.data_ptr(), ws.numel(), _stream(topk_ids))
+          maps.expert_offsets.data_ptr(), ws.data_ptr(), ws.numel(), _stream(index))
     return maps
 
 
-def _tokens(shape, maps, tokens, rows):
-    """Checks token-major and row-major operands (name, tensor) against the shape: (C shape, dtype, device)."""
-    first = (tokens + rows)[0][1]
-    dt, dev = first.dtype, first.device
-    d = _rows_dtype((tokens + rows)[0][0], first)
-    for n, t in tokens:
-        _check(n, t, dt, (shape.T, shape.hidden), dev)
-    for n, t in rows:
-        _check(n, t, dt, (shape.T * shape.kp, shape.hidden), dev)
-    _check("c_map", maps.c_map, torch.int32, (shape.T, shape.kp), dev)
-    return shape.c(d), dt, dev
+def _token_args(shape, name, t, tokens, maps):
+    """(C shape, device index) from a call's first operand, [T, H] (tokens) or [T*k', H]."""
+    index = _index(name, t)
+    d = _rows_dtype(name, t)
+    _check(name, t, t.dtype, (shape.T if tokens else shape.T * shape.kp, shape.hidden), index)
+    _check("c_map", maps.c_map, torch.int32, (shape.T, shape.kp), index)
+    return shape.c(d), index
+
+
+def _operand(name, t, like, rows, hidden, index):
+    """t checked, or an empty [rows, hidden] of the type and device of `like`."""
+    if t is None:
+        return torch.empty((rows, hidden), dtype=like.dtype, device=like.device)
+    _check(name, t, like.dtype, (rows, hidden), index)
+    return t
 
 
 def moe_permute(shape: MoeTokenShape, x, maps: MoeTokenMap, rows=None):
     """x [T, H] -> rows [T*k', H] in expert order; rows from expert_offsets[-1] on are not touched."""
-    s, dt, dev = _tokens(shape, maps, [("x", x)], [("rows", rows)])
-    if rows is None:
-        rows = torch.empty((shape.T * shape.kp, shape.hidden), dtype=dt, device=dev)
-    _call("moe_permute", ctypes.byref(s), x.data_ptr(), maps.c_map.data_ptr(), rows.data_ptr(), _stream(x))
+    s, index = _token_args(shape, "x", x, True, maps)
+    rows = _operand("rows", rows, x, shape.T * shape.kp, shape.hidden, index)
+    _call("moe_permute", ctypes.byref(s), x.data_ptr(), maps.c_map.data_ptr(), rows.data_ptr(), _stream(index))
     return rows
 
 
 def moe_permute_backward(shape: MoeTokenShape, drows, maps: MoeTokenMap, dx=None):
     """Gradient of moe_permute: the sum of each token's rows."""
-    s, dt, dev = _tokens(shape, maps, [("dx", dx)] if dx is not None else [], [("drows", drows)])
-    if dx is None:
-        dx = torch.empty((shape.T, shape.hidden), dtype=dt, device=dev)
+    s, index = _token_args(shape, "drows", drows, False, maps)
+    dx = _operand("dx", dx, drows, shape.T, shape.hidden, index)
     _call("moe_permute_backward", ctypes.byref(s), drows.data_ptr(), maps.c_map.data_ptr(), dx.data_ptr(),
-          _stream(drows))
+          _stream(index))
     return dx
 
 
 def moe_unpermute(shape: MoeTokenShape, rows, topk_w, maps: MoeTokenMap, out=None):
     """rows [T*k', H] in expert order -> out [T, H], weighted with topk_w fp32 [T, k'] and summed per token."""
-    s, dt, dev = _tokens(shape, maps, [("out", out)] if out is not None else [], [("rows", rows)])
-    _check("topk_w", topk_w, torch.float32, (shape.T, shape.kp), dev)
-    if out is None:
-        out = torch.empty((shape.T, shape.hidden), dtype=dt, device=dev)
+    s, index = _token_args(shape, "rows", rows, False, maps)
+    _check("topk_w", topk_w, torch.float32, (shape.T, shape.kp), index)
+    out = _operand("out", out, rows, shape.T, shape.hidden, index)
     _call("moe_unpermute", ctypes.byref(s), rows.data_ptr(), topk_w.data_ptr(), maps.c_map.data_ptr(),
-          out.data_ptr(), _stream(rows))
+          out.data_ptr(), _stream(index))
     return out
 
 
 def moe_unpermute_backward(shape: MoeTokenShape, dout, rows, topk_w, maps: MoeTokenMap, dy=None, dw=None):
     """Gradients of moe_unpermute: (dy [T*k', H] of the rows, dw fp32 [T, k'] of the weights).  dy may be rows;
     rows from expert_offsets[-1] on are not touched."""
-    s, dt, dev = _tokens(shape, maps, [("dout", dout)], [("rows", rows), ("dy", dy)])
-    _check("topk_w", topk_w, torch.float32, (shape.T, shape.kp), dev)
-    _check("dw", dw, torch.float32, (shape.T, shape.kp), dev)
-    if dy is None:
-        dy = torch.empty_like(rows)
+    s, index = _token_args(shape, "dout", dout, True, maps)
+    n = shape.T * shape.kp
+    _check("rows", rows, dout.dtype, (n, shape.hidden), index)
+    _check("topk_w", topk_w, torch.float32, (shape.T, shape.kp), index)
+    dy = _operand("dy", dy, dout, n, shape.hidden, index)
     if dw is None:
         dw = torch.empty_like(topk_w)
+    else:
+        _check("dw", dw, torch.float32, (shape.T, shape.kp), index)
     _call("moe_unpermute_backward", ctypes.byref(s), dout.data_ptr(), rows.data_ptr(), topk_w.data_ptr(),
-          maps.c_map.data_ptr(), dy.data_ptr(), dw.data_ptr(), _stream(rows))
+          maps.c_map.data_ptr(), dy.data_ptr(), dw.data_ptr(), _stream(index))
     return dy, dw
 
 
@@ -304,22 +340,26 @@ def moe_unpermute_backward(shape: MoeTokenShape, dout, rows, topk_w, maps: MoeTo
 def moe_route_backward(shape: MoeTokenShape, topk_ids, topk_w, dtopk_w, shared_logit=None, shared_scale=1.0,
                        dlogits=None, dshared=None):
     """Gradient of moe_route: (dlogits fp32 [T, E_global], dshared fp32 [T, num_shared] or None)."""
-    dev, kp = topk_ids.device, shape.kp
-    _check("topk_ids", topk_ids, torch.int32, (shape.T, kp))
-    _check("topk_w", topk_w, torch.float32, (shape.T, kp), dev)
-    _check("dtopk_w", dtopk_w, torch.float32, (shape.T, kp), dev)
-    _check("dlogits", dlogits, torch.float32, (shape.T, shape.E_global), dev)
-    _check("dshared", dshared, torch.float32, (shape.T, shape.num_shared), dev)
-    _check("shared_logit", shared_logit, torch.bfloat16, (shape.T, shape.num_shared), dev)
+    T, S = shape.T, shape.num_shared
+    picks = (T, shape.kp)
+    index = _index("topk_ids", topk_ids)
+    _check("topk_ids", topk_ids, torch.int32, picks, index)
+    _check("topk_w", topk_w, torch.float32, picks, index)
+    _check("dtopk_w", dtopk_w, torch.float32, picks, index)
+    _check("shared_logit", shared_logit, torch.bfloat16, (T, S), index)
     if dlogits is None:
-        dlogits = torch.empty((shape.T, shape.E_global), dtype=torch.float32, device=dev)
-    if not shape.num_shared:
+        dlogits = torch.empty((T, shape.E_global), dtype=torch.float32, device=topk_ids.device)
+    else:
+        _check("dlogits", dlogits, torch.float32, (T, shape.E_global), index)
+    if not S:
         dshared = None
     elif dshared is None:
-        dshared = torch.empty((shape.T, shape.num_shared), dtype=torch.float32, device=dev)
+        dshared = torch.empty((T, S), dtype=torch.float32, device=topk_ids.device)
+    else:
+        _check("dshared", dshared, torch.float32, (T, S), index)
     s = shape.c()
     _call("moe_route_backward", ctypes.byref(s), _ptr(shared_logit), shared_scale, topk_ids.data_ptr(),
-          topk_w.data_ptr(), dtopk_w.data_ptr(), dlogits.data_ptr(), _ptr(dshared), _stream(topk_ids))
+          topk_w.data_ptr(), dtopk_w.data_ptr(), dlogits.data_ptr(), _ptr(dshared), _stream(index))
     return dlogits, dshared
 
 
@@ -340,21 +380,21 @@ class MoeAdamwTensors:
             raise ValueError("expected lists of one length, got %s" % [len(x) for x in lists])
         self.params, self.grads, self.m, self.v, self.m_scale, self.v_scale = params, grads, m, v, m_scale, v_scale
         self.state = STATE_MXFP8 if mx else STATE_F32
-        self.device = params[0].device if params else torch.device("cuda")
+        self.index = _index("params[0]", params[0]) if params else 0
         g_dtype = grads[0].dtype if grads else torch.float32
         if g_dtype not in (torch.bfloat16, torch.float32):
             raise ValueError("grads: expected bfloat16 or float32, got %s" % g_dtype)
         self.g_dtype = _DTYPES[g_dtype]
         s_dtype = torch.uint8 if mx else torch.float32
         for i, p in enumerate(params):
-            _check("params[%d]" % i, p, torch.float32, None, self.device)
-            _check("grads[%d]" % i, grads[i], g_dtype, p.shape, self.device)
-            _check("m[%d]" % i, m[i], s_dtype, p.shape, self.device)
-            _check("v[%d]" % i, v[i], s_dtype, p.shape, self.device)
+            _check("params[%d]" % i, p, torch.float32, p.shape, self.index)
+            _check("grads[%d]" % i, grads[i], g_dtype, p.shape, self.index)
+            _check("m[%d]" % i, m[i], s_dtype, p.shape, self.index)
+            _check("v[%d]" % i, v[i], s_dtype, p.shape, self.index)
             if mx:
                 blocks = ((p.numel() + 31) // 32,)
-                _check("m_scale[%d]" % i, m_scale[i], torch.uint8, blocks, self.device)
-                _check("v_scale[%d]" % i, v_scale[i], torch.uint8, blocks, self.device)
+                _check("m_scale[%d]" % i, m_scale[i], torch.uint8, blocks, self.index)
+                _check("v_scale[%d]" % i, v_scale[i], torch.uint8, blocks, self.index)
         self._c = (_AdamwTensor * len(params))(*[
             _AdamwTensor(*[x[i].data_ptr() for x in lists], *([] if mx else [None, None]), p.numel())
             for i, p in enumerate(params)])
@@ -377,9 +417,8 @@ def moe_adamw(tensors: MoeAdamwTensors, step: int, lr: float, betas=(0.9, 0.999)
     that multiplies the gradients (not finite: the step is skipped).  seed: of the MXFP8 states' rounding, another
     one each step."""
     if grad_scale is not None:
-        _check("grad_scale", grad_scale, torch.float32, None, tensors.device)
         if grad_scale.numel() != 1:
             raise ValueError("grad_scale: expected one element")
+        _check("grad_scale", grad_scale, torch.float32, grad_scale.shape, tensors.index)
     c = _AdamwConfig(lr, betas[0], betas[1], eps, weight_decay, step, seed, tensors.g_dtype, tensors.state)
-    _call("moe_adamw", tensors._c, len(tensors.params), ctypes.byref(c), _ptr(grad_scale),
-          torch.cuda.current_stream(tensors.device).cuda_stream)
+    _call("moe_adamw", tensors._c, len(tensors.params), ctypes.byref(c), _ptr(grad_scale), _stream(tensors.index))
