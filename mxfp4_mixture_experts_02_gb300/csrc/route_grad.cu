@@ -20,16 +20,24 @@ __global__ void __launch_bounds__(kRgWarps * 32) route_grad_kernel(RouteGradPara
     float* row = reinterpret_cast<float*>(s_rows) + warp * pad;
     for (int e = lane; e < pad; e += 32) row[e] = 0.f;
     __syncwarp();
-    for (int64_t t = static_cast<int64_t>(blockIdx.x) * kRgWarps + warp; t < p.T;
-         t += static_cast<int64_t>(gridDim.x) * kRgWarps) {
-        const int64_t s0 = t * p.kp;
-        int id = -1;
-        float w = 0.f, d = 0.f;
-        if (lane < p.k) {
-            id = p.ids[s0 + lane];
-            w = p.w[s0 + lane];
-            d = p.dw[s0 + lane];
+    const int64_t hop = static_cast<int64_t>(gridDim.x) * kRgWarps;
+    // the next token's picks are on their way while one's row is written
+    int next_id = -1;
+    float next_w = 0.f, next_d = 0.f;
+    auto fetch = [&](int64_t t) {
+        if (t < p.T && lane < p.k) {
+            next_id = p.ids[t * p.kp + lane];
+            next_w = p.w[t * p.kp + lane];
+            next_d = p.dw[t * p.kp + lane];
         }
+    };
+    int64_t t = static_cast<int64_t>(blockIdx.x) * kRgWarps + warp;
+    fetch(t);
+    for (; t < p.T; t += hop) {
+        const int64_t s0 = t * p.kp;
+        const int id = next_id;
+        const float w = next_w, d = next_d;
+        fetch(t + hop);
         float sum = w * d;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);

@@ -10,9 +10,12 @@
 // type).  Sums are in 32 bits, j ascending.  All are bound by the rows they
 // read and write: a token's row is read once, each expert row once.
 //
-// Rows off the 16-byte grid start at different places between its points, so a
-// thread takes a whole piece of what is written (and of what lies like it) and
-// puts the other side's columns together from the two pieces they lie across.
+// Rows off the 16-byte grid: a thread takes a whole piece of the grid in the row
+// that is written and puts the other side's columns together from the two
+// pieces they lie across (the second one comes from L1); the few elements at
+// the row's ends that fill no piece go one by one.
+#include <algorithm>
+
 #include "train.cuh"
 
 namespace moe {
@@ -28,39 +31,57 @@ __device__ __forceinline__ void load_slots(const TokenParams& p, int64_t t, int*
     __syncthreads();
 }
 
-// Bytes sh .. sh + 15 of the pieces a, b; sh in [0, 16), a multiple of 2.
-__device__ __forceinline__ uint4 across(uint4 a, uint4 b, uint32_t sh) {
+// Elements se .. of the pieces a, b: two selections of words, then a shift by
+// half a word.
+template <typename T>
+__device__ __forceinline__ uint4 across(uint4 a, uint4 b, int se) {
+    const uint32_t sh = se * static_cast<uint32_t>(sizeof(T));
     const bool by8 = sh & 8, by4 = sh & 4;
     const uint32_t u0 = by8 ? a.z : a.x, u1 = by8 ? a.w : a.y, u2 = by8 ? b.x : a.z, u3 = by8 ? b.y : a.w,
-                   u4 = by8 ? b.z : b.x, u5 = by8 ? b.w : b.y;
-    const uint32_t v0 = by4 ? u1 : u0, v1 = by4 ? u2 : u1, v2 = by4 ? u3 : u2, v3 = by4 ? u4 : u3, v4 = by4 ? u5 : u4;
-    const uint32_t bits = (sh & 3) * 8;
+                   u4 = by8 ? b.z : b.x;
+    const uint32_t v0 = by4 ? u1 : u0, v1 = by4 ? u2 : u1, v2 = by4 ? u3 : u2, v3 = by4 ? u4 : u3;
+    if constexpr (sizeof(T) == 4) return make_uint4(v0, v1, v2, v3);
+    const uint32_t u5 = by8 ? b.w : b.y, v4 = by4 ? u5 : u4, bits = (sh & 2) * 8;
     return make_uint4(__funnelshift_r(v0, v1, bits), __funnelshift_r(v1, v2, bits), __funnelshift_r(v2, v3, bits),
                       __funnelshift_r(v3, v4, bits));
 }
 
-// kVe elements from element e on, all of which are in the tensor of `total`
-// elements (which starts on the grid).
+// A row as `head` single elements, n accesses and `tail` single elements.
+struct Cut {
+    int head, n, tail;
+    // column of the i-th single element
+    __device__ __forceinline__ int single(int i, int cols) const { return i < head ? i : cols - tail + i - head; }
+};
+
+template <typename T, int LIE>
+__device__ __forceinline__ Cut cut_row(int64_t first, int cols) {
+    constexpr int VE = kVe<T, LIE>;
+    if (LIE != kOff) return Cut{0, cols / VE, 0};
+    const int head = min(cols, static_cast<int>(-first & (VE - 1)));
+    return Cut{head, (cols - head) / VE, (cols - head) % VE};
+}
+
+// kVe elements from element e on, all of them in the tensor of `total` elements
+// (which starts on the grid).
 template <typename T, int LIE>
 __device__ __forceinline__ void load_from(Vec<T, kVe<T, LIE>>& v, const T* tensor, int64_t e, int64_t total) {
     if constexpr (LIE == kOff) {
         constexpr int VE = kFull<T>;
-        const int64_t piece = e / VE * VE;
-        const int se = static_cast<int>(e - piece);
+        const int se = static_cast<int>(e & (VE - 1));
         Vec<T, VE> a, b;
-        a.load(tensor + piece);
+        a.load(tensor + e - se);
         b.w = a.w;
         if (se) {
-            if (piece + 2 * VE <= total) {
-                b.load(tensor + piece + VE);
+            if (e - se + 2 * VE <= total) {
+                b.load(tensor + e - se + VE);
             } else {  // the tensor ends inside the second piece
                 float f[VE];
 #pragma unroll
-                for (int u = 0; u < VE; ++u) f[u] = piece + VE + u < total ? to_f32(tensor[piece + VE + u]) : 0.f;
+                for (int u = 0; u < VE; ++u) f[u] = e - se + VE + u < total ? to_f32(tensor[e - se + VE + u]) : 0.f;
                 b.set(f);
             }
         }
-        v.w = across(a.w, b.w, se * static_cast<uint32_t>(sizeof(T)));
+        v.w = across<T>(a.w, b.w, se);
     } else {
         v.load(tensor + e);
     }
@@ -72,27 +93,32 @@ template <typename T, int LIE>
 __global__ void __launch_bounds__(kTokThreads) permute_kernel(TokenParams p) {
     constexpr int VE = kVe<T, LIE>;
     __shared__ int s_row[kMaxSlots];
-    const int64_t t = blockIdx.x, total = static_cast<int64_t>(p.T) * p.H;
+    const int64_t t = blockIdx.x, total = static_cast<int64_t>(p.T) * p.H, row = t * p.H;
     load_slots(p, t, s_row);
     const T* src = static_cast<const T*>(p.src);
-    const int c0 = (blockIdx.y * kTokThreads + threadIdx.x) * VE;
+    const int i = blockIdx.y * kTokThreads + threadIdx.x;  // this thread's access, and single element
     Vec<T, VE> v;
     if (LIE != kOff) {
-        if (c0 >= p.H) return;
-        v.load(src + t * p.H + c0);
+        if (i * VE >= p.H) return;
+        v.load(src + row + i * VE);
     }
     for (int j = 0; j < p.kp; ++j) {
         const int64_t r = s_row[j];
         if (r < 0) continue;
-        const int c = c0 - before<T, LIE>(r * p.H);
-        T* dst = static_cast<T*>(p.dst) + r * p.H + c;
-        if (whole<T, LIE>(c, p.H)) {
-            if (LIE == kOff) load_from<T, LIE>(v, src, t * p.H + c, total);
-            v.store(dst);
-        } else if (LIE == kOff) {
-#pragma unroll
-            for (int u = 0; u < VE; ++u)
-                if (c + u >= 0 && c + u < p.H) dst[u] = src[t * p.H + c + u];
+        T* dst = static_cast<T*>(p.dst) + r * p.H;
+        if (LIE != kOff) {
+            v.store(dst + i * VE);
+            continue;
+        }
+        const Cut cut = cut_row<T, LIE>(r * p.H, p.H);
+        if (i < cut.n) {
+            const int c = cut.head + i * VE;
+            load_from<T, LIE>(v, src, row + c, total);
+            v.store(dst + c);
+        }
+        if (i < cut.head + cut.tail) {
+            const int c = cut.single(i, p.H);
+            dst[c] = src[row + c];
         }
     }
 }
@@ -108,13 +134,14 @@ __global__ void __launch_bounds__(kTokThreads) unpermute_kernel(TokenParams p) {
     if (threadIdx.x < p.kp) s_w[threadIdx.x] = p.w ? p.w[t * p.kp + threadIdx.x] : 1.f;
     load_slots(p, t, s_row);
     const T* src = static_cast<const T*>(p.src);
-    const int c = (blockIdx.y * kTokThreads + threadIdx.x) * VE - before<T, LIE>(t * p.H);
-    if (c >= p.H) return;
-    float acc[VE];
+    T* dst = static_cast<T*>(p.dst) + t * p.H;
+    const int i = blockIdx.y * kTokThreads + threadIdx.x;
+    const Cut cut = cut_row<T, LIE>(t * p.H, p.H);
+    if (i < cut.n) {
+        const int c = cut.head + i * VE;
+        float acc[VE];
 #pragma unroll
-    for (int u = 0; u < VE; ++u) acc[u] = 0.f;
-    T* dst = static_cast<T*>(p.dst) + t * p.H + c;
-    if (whole<T, LIE>(c, p.H)) {
+        for (int u = 0; u < VE; ++u) acc[u] = 0.f;
         for (int j0 = 0; j0 < p.kp; j0 += kRowBatch) {
             Vec<T, VE> v[kRowBatch];
 #pragma unroll
@@ -133,109 +160,85 @@ __global__ void __launch_bounds__(kTokThreads) unpermute_kernel(TokenParams p) {
         }
         Vec<T, VE> o;
         o.set(acc);
-        o.store(dst);
-    } else if (LIE == kOff) {
+        o.store(dst + c);
+    }
+    if (LIE == kOff && i < cut.head + cut.tail) {
+        const int c = cut.single(i, p.H);
+        float acc = 0.f;
         for (int j = 0; j < p.kp; ++j) {
             const int64_t r = s_row[j];
-            if (r < 0) continue;
-#pragma unroll
-            for (int u = 0; u < VE; ++u)
-                if (c + u >= 0 && c + u < p.H) acc[u] += s_w[j] * to_f32(src[r * p.H + c + u]);
+            if (r >= 0) acc += s_w[j] * to_f32(src[r * p.H + c]);
         }
-#pragma unroll
-        for (int u = 0; u < VE; ++u)
-            if (c + u >= 0 && c + u < p.H) dst[u] = from_f32<T>(acc[u]);
+        dst[c] = from_f32<T>(acc);
     }
 }
 
-constexpr int kGradTokThreads = 256;
+constexpr int kSlotWarps = 8;
 
-// CTA (token, group of `per` slots): a routing weight's gradient is a sum over
-// the whole row, the warps' parts of it gather in shared memory.
+// A warp per slot: it walks over the row once, so the routing weight's gradient
+// (a sum over the whole row) needs one reduction and no barrier; the token's
+// row comes from L1 for all its slots but the first.
 template <typename T, int LIE>
-__global__ void __launch_bounds__(kGradTokThreads) unpermute_grad_kernel(TokenParams p, int per) {
-    constexpr int VE = kVe<T, LIE>, kWarps = kGradTokThreads / 32;
-    __shared__ int s_row[kMaxSlots];
-    __shared__ float s_w[kMaxSlots];
-    __shared__ float s_dot[kMaxSlots][kWarps];
-    const int64_t t = blockIdx.x, total = static_cast<int64_t>(p.T) * p.H;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int j_begin = blockIdx.y * per, j_end = min(p.kp, j_begin + per);
-    const T *src = static_cast<const T*>(p.src), *dout = static_cast<const T*>(p.dout);
-    if (threadIdx.x < p.kp) s_w[threadIdx.x] = p.w[t * p.kp + threadIdx.x];
-    for (int i = threadIdx.x; i < kMaxSlots * kWarps; i += kGradTokThreads) s_dot[i / kWarps][i % kWarps] = 0.f;
-    load_slots(p, t, s_row);
-    const int span = p.H + (LIE == kOff ? VE - 1 : 0);
-    for (int c0 = threadIdx.x * VE; c0 - static_cast<int>(threadIdx.x) * VE < span; c0 += kGradTokThreads * VE) {
-        float d[VE];
-        if (LIE != kOff) {
+__global__ void __launch_bounds__(kSlotWarps * 32) unpermute_grad_kernel(TokenParams p) {
+    constexpr int VE = kVe<T, LIE>;
+    constexpr int kBatch = LIE == kOff ? 1 : 4;  // accesses in flight; off the grid each takes registers enough
+    const int64_t slot = static_cast<int64_t>(blockIdx.x) * kSlotWarps + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
+    const int64_t slots = static_cast<int64_t>(p.T) * p.kp, total = static_cast<int64_t>(p.T) * p.H;
+    if (slot >= slots) return;
+    const int64_t t = slot / p.kp, r = p.c_map[slot];
+    if (r < 0) {
+        if (lane == 0) p.dw[slot] = 0.f;
+        return;
+    }
+    const float w = p.w[slot];
+    const int64_t from = t * p.H, to = r * p.H;
+    const T *src = static_cast<const T*>(p.src) + to, *dout = static_cast<const T*>(p.dout);
+    T* dst = static_cast<T*>(p.dst) + to;
+    const Cut cut = cut_row<T, LIE>(to, p.H);
+    float dot = 0.f;
+#pragma unroll 1
+    for (int i0 = lane; i0 < cut.n; i0 += 32 * kBatch) {
+        Vec<T, VE> y[kBatch], g[kBatch];
 #pragma unroll
-            for (int u = 0; u < VE; ++u) d[u] = 0.f;
-            if (c0 < p.H) {
-                Vec<T, VE> v;
-                v.load(dout + t * p.H + c0);
-                v.get(d);
+        for (int b = 0; b < kBatch; ++b) {
+            const int c = cut.head + (i0 + 32 * b) * VE;
+            if (i0 + 32 * b < cut.n) {
+                y[b].load(src + c);
+                load_from<T, LIE>(g[b], dout, from + c, total);
             }
         }
-        for (int j0 = j_begin; j0 < j_end; j0 += kRowBatch) {
-            Vec<T, VE> y[kRowBatch];
-            int c[kRowBatch];
 #pragma unroll
-            for (int b = 0; b < kRowBatch; ++b) {
-                const int64_t r = j0 + b < j_end ? s_row[j0 + b] : -1;
-                c[b] = c0 - (r >= 0 ? before<T, LIE>(r * p.H) : 0);
-                if (r >= 0 && whole<T, LIE>(c[b], p.H)) y[b].load(src + r * p.H + c[b]);
+        for (int b = 0; b < kBatch; ++b) {
+            if (i0 + 32 * b >= cut.n) continue;
+            float f[VE], d[VE];
+            y[b].get(f);
+            g[b].get(d);
+#pragma unroll
+            for (int u = 0; u < VE; ++u) {
+                dot += d[u] * f[u];
+                f[u] = w * d[u];
             }
-#pragma unroll
-            for (int b = 0; b < kRowBatch; ++b) {
-                const int64_t r = j0 + b < j_end ? s_row[j0 + b] : -1;
-                if (r < 0) continue;  // the same for the whole CTA
-                const float w = s_w[j0 + b];
-                float dot = 0.f;
-                T* dst = static_cast<T*>(p.dst) + r * p.H + c[b];
-                if (whole<T, LIE>(c[b], p.H)) {
-                    float f[VE];
-                    Vec<T, VE> o;
-                    if (LIE == kOff) {
-                        load_from<T, LIE>(o, dout, t * p.H + c[b], total);
-                        o.get(d);
-                    }
-                    y[b].get(f);
-#pragma unroll
-                    for (int u = 0; u < VE; ++u) {
-                        dot += d[u] * f[u];
-                        f[u] = w * d[u];
-                    }
-                    o.set(f);
-                    o.store(dst);
-                } else if (LIE == kOff) {
-#pragma unroll
-                    for (int u = 0; u < VE; ++u)
-                        if (c[b] + u >= 0 && c[b] + u < p.H) {
-                            const float g = to_f32(dout[t * p.H + c[b] + u]);
-                            dot += g * to_f32(src[r * p.H + c[b] + u]);
-                            dst[u] = from_f32<T>(w * g);
-                        }
-                }
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-                if (lane == 0) s_dot[j0 + b][warp] += dot;
-            }
+            y[b].set(f);
+            y[b].store(dst + cut.head + (i0 + 32 * b) * VE);
         }
     }
-    __syncthreads();
-    const int j = j_begin + threadIdx.x;
-    if (j < j_end) {
-        float s = 0.f;
-#pragma unroll
-        for (int i = 0; i < kWarps; ++i) s += s_dot[j][i];
-        p.dw[t * p.kp + j] = s;
+    if (LIE == kOff && lane < cut.head + cut.tail) {
+        const int c = cut.single(lane, p.H);
+        const float d = to_f32(dout[from + c]);
+        dot += d * to_f32(src[c]);
+        dst[c] = from_f32<T>(w * d);
     }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+    if (lane == 0) p.dw[slot] = dot;
 }
 
 template <typename T, int LIE>
 dim3 token_grid(const TokenParams& p) {
-    return dim3(p.T, (accesses<T, LIE>(p.H) + kTokThreads - 1) / kTokThreads);
+    // off the grid at least one chunk, for the single elements of a short row
+    const int n = LIE == kOff ? std::max(1, p.H / kVe<T, LIE>) : p.H / kVe<T, LIE>;
+    return dim3(p.T, (n + kTokThreads - 1) / kTokThreads);
 }
 
 }  // namespace
@@ -256,11 +259,11 @@ cudaError_t launch_unpermute(const TokenParams& p, int dtype, int lie, cudaStrea
 }
 
 cudaError_t launch_unpermute_grad(const TokenParams& p, int dtype, int lie, cudaStream_t st) {
-    // few tokens: a CTA for each batch of slots
-    const int per = p.T < 2 * kSms ? kRowBatch : p.kp;
+    const int64_t slots = static_cast<int64_t>(p.T) * p.kp;
     return by_type(dtype, lie, [&](auto t, auto l) {
-        return launch_kernel(unpermute_grad_kernel<decltype(t), l.value>, dim3(p.T, (p.kp + per - 1) / per),
-                             dim3(kGradTokThreads), 0, st, false, p, per);
+        return launch_kernel(unpermute_grad_kernel<decltype(t), l.value>,
+                             dim3(static_cast<unsigned>((slots + kSlotWarps - 1) / kSlotWarps)), dim3(kSlotWarps * 32),
+                             0, st, false, p);
     });
 }
 
