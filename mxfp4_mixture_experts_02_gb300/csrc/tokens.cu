@@ -62,30 +62,40 @@ __device__ __forceinline__ Cut cut_row(int64_t first, int cols) {
 }
 
 // kVe elements from element e on, all of them in the tensor of `total` elements
-// (which starts on the grid).
+// (which starts on the grid): issue() sends the loads on their way, without a
+// branch, take() puts the elements together.
 template <typename T, int LIE>
-__device__ __forceinline__ void load_from(Vec<T, kVe<T, LIE>>& v, const T* tensor, int64_t e, int64_t total) {
-    if constexpr (LIE == kOff) {
-        constexpr int VE = kFull<T>;
-        const int se = static_cast<int>(e & (VE - 1));
-        Vec<T, VE> a, b;
-        a.load(tensor + e - se);
-        b.w = a.w;
-        if (se) {
-            if (e - se + 2 * VE <= total) {
-                b.load(tensor + e - se + VE);
-            } else {  // the tensor ends inside the second piece
+struct Source {
+    static constexpr int VE = kVe<T, LIE>;
+    Vec<T, VE> a;
+    Vec<T, LIE == kOff ? VE : 1> b;
+    __device__ __forceinline__ void issue(const T* tensor, int64_t e, int64_t total) {
+        if constexpr (LIE == kOff) {
+            const int se = static_cast<int>(e & (VE - 1));
+            const T* piece = tensor + (e - se);
+            a.load(piece);
+            b.load(se && e - se + 2 * VE <= total ? piece + VE : piece);
+        } else {
+            a.load(tensor + e);
+        }
+    }
+    __device__ __forceinline__ Vec<T, VE> take(const T* tensor, int64_t e, int64_t total) {
+        if constexpr (LIE == kOff) {
+            const int se = static_cast<int>(e & (VE - 1));
+            if (e - se + 2 * VE > total && se) {  // the tensor ends inside the second piece
                 float f[VE];
 #pragma unroll
                 for (int u = 0; u < VE; ++u) f[u] = e - se + VE + u < total ? to_f32(tensor[e - se + VE + u]) : 0.f;
                 b.set(f);
             }
+            Vec<T, VE> v;
+            v.w = across<T>(a.w, b.w, se);
+            return v;
+        } else {
+            return a;
         }
-        v.w = across<T>(a.w, b.w, se);
-    } else {
-        v.load(tensor + e);
     }
-}
+};
 
 // CTA (token, chunk of columns): the chunk is read once (off the grid, again
 // from L1 for each row) and written to the token's rows.
@@ -113,7 +123,9 @@ __global__ void __launch_bounds__(kTokThreads) permute_kernel(TokenParams p) {
         const Cut cut = cut_row<T, LIE>(r * p.H, p.H);
         if (i < cut.n) {
             const int c = cut.head + i * VE;
-            load_from<T, LIE>(v, src, row + c, total);
+            Source<T, LIE> x;
+            x.issue(src, row + c, total);
+            v = x.take(src, row + c, total);
             v.store(dst + c);
         }
         if (i < cut.head + cut.tail) {
@@ -130,39 +142,68 @@ __global__ void __launch_bounds__(kTokThreads) unpermute_kernel(TokenParams p) {
     constexpr int VE = kVe<T, LIE>;
     __shared__ int s_row[kMaxSlots];
     __shared__ float s_w[kMaxSlots];
+    const int64_t t = blockIdx.x;
+    if (threadIdx.x < p.kp) s_w[threadIdx.x] = p.w ? p.w[t * p.kp + threadIdx.x] : 1.f;
+    load_slots(p, t, s_row);
+    const int c = (blockIdx.y * kTokThreads + threadIdx.x) * VE;
+    if (c >= p.H) return;
+    float acc[VE];
+#pragma unroll
+    for (int u = 0; u < VE; ++u) acc[u] = 0.f;
+    for (int j0 = 0; j0 < p.kp; j0 += kRowBatch) {
+        Vec<T, VE> v[kRowBatch];
+#pragma unroll
+        for (int b = 0; b < kRowBatch; ++b) {
+            const int64_t r = j0 + b < p.kp ? s_row[j0 + b] : -1;
+            if (r >= 0) v[b].load(static_cast<const T*>(p.src) + r * p.H + c);
+        }
+#pragma unroll
+        for (int b = 0; b < kRowBatch; ++b) {
+            if (j0 + b >= p.kp || s_row[j0 + b] < 0) continue;  // a slot without a row adds nothing
+            float f[VE];
+            v[b].get(f);
+#pragma unroll
+            for (int u = 0; u < VE; ++u) acc[u] += s_w[j0 + b] * f[u];
+        }
+    }
+    Vec<T, VE> o;
+    o.set(acc);
+    o.store(static_cast<T*>(p.dst) + t * p.H + c);
+}
+
+// Off the grid: the pieces that a chunk's rows lie in come into shared memory
+// on their own, all slots' at once, and each thread puts its columns of a row
+// together from two of them.
+template <typename T>
+__global__ void __launch_bounds__(kTokThreads) unpermute_off_kernel(TokenParams p) {
+    constexpr int VE = kFull<T>;
+    constexpr int kRow = (kTokThreads + 1) * 16;  // bytes of a slot's pieces
+    extern __shared__ uint4 s_piece[];
+    __shared__ int s_row[kMaxSlots];
+    __shared__ float s_w[kMaxSlots];
     const int64_t t = blockIdx.x, total = static_cast<int64_t>(p.T) * p.kp * p.H;
     if (threadIdx.x < p.kp) s_w[threadIdx.x] = p.w ? p.w[t * p.kp + threadIdx.x] : 1.f;
     load_slots(p, t, s_row);
     const T* src = static_cast<const T*>(p.src);
     T* dst = static_cast<T*>(p.dst) + t * p.H;
-    const int i = blockIdx.y * kTokThreads + threadIdx.x;
-    const Cut cut = cut_row<T, LIE>(t * p.H, p.H);
-    if (i < cut.n) {
-        const int c = cut.head + i * VE;
-        float acc[VE];
-#pragma unroll
-        for (int u = 0; u < VE; ++u) acc[u] = 0.f;
-        for (int j0 = 0; j0 < p.kp; j0 += kRowBatch) {
-            Vec<T, VE> v[kRowBatch];
-#pragma unroll
-            for (int b = 0; b < kRowBatch; ++b) {
-                const int64_t r = j0 + b < p.kp ? s_row[j0 + b] : -1;
-                if (r >= 0) load_from<T, LIE>(v[b], src, r * p.H + c, total);
-            }
-#pragma unroll
-            for (int b = 0; b < kRowBatch; ++b) {
-                if (j0 + b >= p.kp || s_row[j0 + b] < 0) continue;  // a slot without a row adds nothing
-                float f[VE];
-                v[b].get(f);
-#pragma unroll
-                for (int u = 0; u < VE; ++u) acc[u] += s_w[j0 + b] * f[u];
-            }
+    const Cut cut = cut_row<T, kOff>(t * p.H, p.H);
+    const int i0 = blockIdx.y * kTokThreads, i = i0 + threadIdx.x;
+    const int n = min(cut.n - i0, kTokThreads);  // accesses of the chunk
+    const int c0 = cut.head + i0 * VE;
+    const uint32_t mine = ptx::smem_u32(s_piece) + threadIdx.x * 16;
+    for (int j = 0; j < p.kp; ++j) {
+        const int64_t r = s_row[j];
+        if (r < 0) continue;
+        const int64_t e = r * p.H + c0, first = e & ~static_cast<int64_t>(VE - 1);
+        const int pieces = n + (e != first);
+        for (int k = threadIdx.x; k < pieces; k += kTokThreads) {
+            const int64_t at = first + static_cast<int64_t>(k) * VE;  // the tensor may end in the last piece
+            ptx::cp_async_16_part(mine + j * kRow + (k - static_cast<int>(threadIdx.x)) * 16, src + at,
+                                  static_cast<uint32_t>(min(static_cast<int64_t>(VE), total - at) * sizeof(T)));
         }
-        Vec<T, VE> o;
-        o.set(acc);
-        o.store(dst + c);
     }
-    if (LIE == kOff && i < cut.head + cut.tail) {
+    // the row's single elements meanwhile
+    if (i < cut.head + cut.tail) {
         const int c = cut.single(i, p.H);
         float acc = 0.f;
         for (int j = 0; j < p.kp; ++j) {
@@ -171,6 +212,28 @@ __global__ void __launch_bounds__(kTokThreads) unpermute_kernel(TokenParams p) {
         }
         dst[c] = from_f32<T>(acc);
     }
+    ptx::cp_async_wait_all();
+    __syncthreads();
+    if (static_cast<int>(threadIdx.x) >= n) return;
+    float acc[VE];
+#pragma unroll
+    for (int u = 0; u < VE; ++u) acc[u] = 0.f;
+    for (int j = 0; j < p.kp; ++j) {
+        const int64_t r = s_row[j];
+        if (r < 0) continue;  // a slot without a row adds nothing
+        const int se = static_cast<int>((r * p.H + c0) & (VE - 1));
+        const uint4 a = ptx::ld_shared_16(mine + j * kRow);
+        const uint4 b = se ? ptx::ld_shared_16(mine + j * kRow + 16) : a;
+        Vec<T, VE> v;
+        float f[VE];
+        v.w = across<T>(a, b, se);
+        v.get(f);
+#pragma unroll
+        for (int u = 0; u < VE; ++u) acc[u] += s_w[j] * f[u];
+    }
+    Vec<T, VE> o;
+    o.set(acc);
+    o.store(dst + c0 + threadIdx.x * VE);
 }
 
 constexpr int kSlotWarps = 8;
@@ -199,13 +262,14 @@ __global__ void __launch_bounds__(kSlotWarps * 32) unpermute_grad_kernel(TokenPa
     float dot = 0.f;
 #pragma unroll 1
     for (int i0 = lane; i0 < cut.n; i0 += 32 * kBatch) {
-        Vec<T, VE> y[kBatch], g[kBatch];
+        Vec<T, VE> y[kBatch];
+        Source<T, LIE> g[kBatch];
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {
             const int c = cut.head + (i0 + 32 * b) * VE;
             if (i0 + 32 * b < cut.n) {
                 y[b].load(src + c);
-                load_from<T, LIE>(g[b], dout, from + c, total);
+                g[b].issue(dout, from + c, total);
             }
         }
 #pragma unroll
@@ -213,7 +277,7 @@ __global__ void __launch_bounds__(kSlotWarps * 32) unpermute_grad_kernel(TokenPa
             if (i0 + 32 * b >= cut.n) continue;
             float f[VE], d[VE];
             y[b].get(f);
-            g[b].get(d);
+            g[b].take(dout, from + cut.head + (i0 + 32 * b) * VE, total).get(d);
 #pragma unroll
             for (int u = 0; u < VE; ++u) {
                 dot += d[u] * f[u];
@@ -253,8 +317,17 @@ cudaError_t launch_permute(const TokenParams& p, int dtype, int lie, cudaStream_
 cudaError_t launch_unpermute(const TokenParams& p, int dtype, int lie, cudaStream_t st) {
     return by_type(dtype, lie, [&](auto t, auto l) {
         using T = decltype(t);
-        return launch_kernel(unpermute_kernel<T, l.value>, token_grid<T, l.value>(p), dim3(kTokThreads), 0, st, false,
-                             p);
+        if constexpr (l.value == kOff) {
+            const size_t smem = static_cast<size_t>(p.kp) * (kTokThreads + 1) * 16;  // at most 68 KB
+            const cudaError_t e = cudaFuncSetAttribute(
+                unpermute_off_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+            if (e != cudaSuccess) return e;
+            return launch_kernel(unpermute_off_kernel<T>, token_grid<T, l.value>(p), dim3(kTokThreads), smem, st, false,
+                                 p);
+        } else {
+            return launch_kernel(unpermute_kernel<T, l.value>, token_grid<T, l.value>(p), dim3(kTokThreads), 0, st,
+                                 false, p);
+        }
     });
 }
 
