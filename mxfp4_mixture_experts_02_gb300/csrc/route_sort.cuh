@@ -303,5 +303,22 @@ __device__ __forceinline__ void place_experts(const SortParams& p, int cnt, int*
     }
 }
 
+// The lanes of the warp holding the same local expert as this lane (the
+// mask match.any returns), from one ballot per bit: e in [-1, 1023] is taken
+// as 11 bits (-1 -> 2047) and a lane matches where every bit agrees.  Eleven
+// ballots cost far less than match.any over 32 distinct experts (on GB300
+// a count round went from ~1400 to ~100 cycles).
+__device__ __forceinline__ uint32_t same_expert_lanes(int e) {
+    const uint32_t v = static_cast<uint32_t>(e) & 2047u;
+    uint32_t m = 0xffffffffu;
+#pragma unroll
+    for (int b = 0; b < 11; ++b) {
+        const bool bit = (v >> b) & 1u;
+        const uint32_t x = __ballot_sync(0xffffffffu, bit);
+        m &= bit ? x : ~x;
+    }
+    return m;
+}
+
 }  // namespace rs
 }  // namespace moe

@@ -31,27 +31,11 @@ constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 using rs::local_expert;
 using rs::place_experts;
+using rs::same_expert_lanes;
 
 constexpr int kBigWarps = 8;
 constexpr int kBigWarpSlots = 512;
 constexpr int kBigRounds = kBigWarpSlots / 32;
-
-// The lanes of the warp holding the same local expert as this lane (the
-// mask match.any returns), from one ballot per bit: e in [-1, 1023] is taken
-// as 11 bits (-1 -> 2047) and a lane matches where every bit agrees.  Eleven
-// ballots cost far less than match.any over 32 distinct experts (on GB300
-// a count round went from ~1400 to ~100 cycles).
-__device__ __forceinline__ uint32_t same_expert_lanes(int e) {
-    const uint32_t v = static_cast<uint32_t>(e) & 2047u;
-    uint32_t m = 0xffffffffu;
-#pragma unroll
-    for (int b = 0; b < 11; ++b) {
-        const bool bit = (v >> b) & 1u;
-        const uint32_t x = __ballot_sync(0xffffffffu, bit);
-        m &= bit ? x : ~x;
-    }
-    return m;
-}
 
 // The local experts of a warp's kBigWarpSlots slots [s0, s1), round r in
 // e[r] (lane = slot within the round; -1 past s1 or without a local row).

@@ -218,6 +218,9 @@ struct TokenParams {
     int T, kp, H;
 };
 
+// Slots sorted by expert (of p: ids, offsets, a_map, c_map and, for long
+// batches, the sort's other tables).
+cudaError_t launch_token_map(const SortParams& p, cudaStream_t st);
 cudaError_t launch_permute(const TokenParams& p, int dtype, int lie, cudaStream_t st);
 cudaError_t launch_unpermute(const TokenParams& p, int dtype, int lie, cudaStream_t st);
 cudaError_t launch_unpermute_grad(const TokenParams& p, int dtype, int lie, cudaStream_t st);

@@ -226,7 +226,7 @@ int moe_token_map(const moe_token_shape* s, const int32_t* ids, int32_t* a_map, 
     p.G = 1;
     p.H = s->hidden;
     p.gemm2_force = MOE_GEMM2_SPLIT;
-    return rc_of(launch_sort(p, cu(stream), false));
+    return rc_of(launch_token_map(p, cu(stream)));
 }
 
 int moe_permute(const moe_token_shape* s, const void* x, const int32_t* c_map, void* rows, moe_stream_t stream) {
