@@ -21,9 +21,12 @@ namespace {
 
 constexpr int kAdamwThreads = 256;
 constexpr int kE = 8;  // elements per thread: four threads share a block of 32
-// Resident CTAs: as many as hold two steps' reads in registers.
+// Resident CTAs.  With fp32 states two keep memory busy (128 M parameters: 505
+// us, 522 with four); with MXFP8 states the update has about as many
+// instructions as its bytes allow time for, and four hide its latencies better
+// than registers that would hold the next step (96 M: 257 us, 262 with three).
 template <bool MX>
-constexpr uint32_t kAdamwCtas = MX ? 3 : 2;
+constexpr uint32_t kAdamwCtas = MX ? 4 : 2;
 constexpr uint64_t kGamma = 0x9E3779B97F4A7C15ull;
 
 // SplitMix64's output function at state z.
@@ -262,6 +265,17 @@ __device__ __forceinline__ void fetch(Step<G, MX>& s, const ItemPtrs<G>& t, uint
     }
 }
 
+// A step's lines into L2, by the threads whose elements begin them.
+template <typename G>
+__device__ __forceinline__ void prefetch(const ItemPtrs<G>& t, uint32_t o) {
+    if (threadIdx.x % 4 == 0) ptx::prefetch_l2(t.p + o);
+    if (threadIdx.x % (16 / sizeof(G)) == 0) ptx::prefetch_l2(t.g + o);
+    if (threadIdx.x % 16 == 0) {
+        ptx::prefetch_l2(static_cast<const uint8_t*>(t.m) + o);
+        ptx::prefetch_l2(static_cast<const uint8_t*>(t.v) + o);
+    }
+}
+
 // The update of a step's elements, and their writes.
 template <bool FULL, typename G, bool MX, typename B>
 __device__ __forceinline__ void update(const Step<G, MX>& s, const B& b, const ItemPtrs<G>& t, uint32_t o, int live,
@@ -369,22 +383,14 @@ __global__ void __launch_bounds__(kAdamwThreads, kAdamwCtas<MX>) adamw_kernel(co
         const bool by32 = t.vec == 2;
         int done = 0;
         const uint32_t mine = threadIdx.x * kE;
-        if (t.vec && size >= kAdamwStep) {
-            // the next step's reads are on their way during one
-            Step<G, MX> s0, s1;
-            const int full = size / kAdamwStep * kAdamwStep;
-            fetch<true>(s0, q, mine, kE, by32);
-            for (; done < full; done += 2 * kAdamwStep) {
-                const uint32_t o0 = done + mine, o1 = o0 + kAdamwStep, o2 = o1 + kAdamwStep;
-                if (done + kAdamwStep < full) fetch<true>(s1, q, o1, kE, by32);
-                update<true>(s0, b, q, o0, kE, by32, clip);
-                if (done + kAdamwStep < full) {
-                    if (done + 2 * kAdamwStep < full) fetch<true>(s0, q, o2, kE, by32);
-                    update<true>(s1, b, q, o1, kE, by32, clip);
-                }
+        if (t.vec)
+            for (; done + kAdamwStep <= size; done += kAdamwStep) {
+                const uint32_t o = done + mine;
+                Step<G, MX> s;
+                fetch<true>(s, q, o, kE, by32);
+                if (MX && done + 3 * kAdamwStep <= size) prefetch(q, o + 2 * kAdamwStep);
+                update<true>(s, b, q, o, kE, by32, clip);
             }
-            done = full;
-        }
         for (; done < size; done += kAdamwStep) {
             const int o = done + static_cast<int>(mine), live = max(0, min(size - o, kE));
             Step<G, MX> s;
