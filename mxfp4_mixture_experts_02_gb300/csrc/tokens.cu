@@ -178,62 +178,67 @@ template <typename T>
 __global__ void __launch_bounds__(kTokThreads) unpermute_off_kernel(TokenParams p) {
     constexpr int VE = kFull<T>;
     constexpr int kRow = (kTokThreads + 1) * 16;  // bytes of a slot's pieces
+    struct alignas(16) Slot {
+        const T* piece;  // the first one that the chunk lies in
+        int bytes;       // from there to the tensor's end, as far as the chunk may reach
+        int se;          // of the chunk's first column in that piece; -1 for a slot without a row
+    };
     extern __shared__ uint4 s_piece[];
-    __shared__ int s_row[kMaxSlots];
+    __shared__ Slot s_slot[kMaxSlots];
     __shared__ float s_w[kMaxSlots];
-    const int64_t t = blockIdx.x, total = static_cast<int64_t>(p.T) * p.kp * p.H;
-    if (threadIdx.x < p.kp) s_w[threadIdx.x] = p.w ? p.w[t * p.kp + threadIdx.x] : 1.f;
-    load_slots(p, t, s_row);
+    const int64_t t = blockIdx.x;
     const T* src = static_cast<const T*>(p.src);
     T* dst = static_cast<T*>(p.dst) + t * p.H;
     const Cut cut = cut_row<T, kOff>(t * p.H, p.H);
-    const int i0 = blockIdx.y * kTokThreads, i = i0 + threadIdx.x;
+    const int i0 = blockIdx.y * kTokThreads, tid = threadIdx.x;
     const int n = min(cut.n - i0, kTokThreads);  // accesses of the chunk
     const int c0 = cut.head + i0 * VE;
-    const uint32_t mine = ptx::smem_u32(s_piece) + threadIdx.x * 16;
+    if (tid < p.kp) {
+        const int64_t r = p.c_map[t * p.kp + tid], e = r * p.H + c0, total = static_cast<int64_t>(p.T) * p.kp * p.H;
+        const int se = static_cast<int>(e & (VE - 1));
+        s_w[tid] = p.w ? p.w[t * p.kp + tid] : 1.f;
+        s_slot[tid] = Slot{src + (e - se),
+                           static_cast<int>(min(total - (e - se), static_cast<int64_t>(kRow)) * sizeof(T)),
+                           r < 0 ? -1 : se};
+    }
+    __syncthreads();
+    const uint32_t mine = ptx::smem_u32(s_piece) + tid * 16;
     for (int j = 0; j < p.kp; ++j) {
-        const int64_t r = s_row[j];
-        if (r < 0) continue;
-        const int64_t e = r * p.H + c0, first = e & ~static_cast<int64_t>(VE - 1);
-        const int pieces = n + (e != first);
-        for (int k = threadIdx.x; k < pieces; k += kTokThreads) {
-            const int64_t at = first + static_cast<int64_t>(k) * VE;  // the tensor may end in the last piece
-            ptx::cp_async_16_part(mine + j * kRow + (k - static_cast<int>(threadIdx.x)) * 16, src + at,
-                                  static_cast<uint32_t>(min(static_cast<int64_t>(VE), total - at) * sizeof(T)));
-        }
+        const Slot s = s_slot[j];
+        const int pieces = n + (s.se > 0);
+        if (s.se < 0 || tid >= pieces) continue;
+        ptx::cp_async_16_part(mine + j * kRow, s.piece + tid * VE, min(s.bytes - tid * 16, 16));
+        if (tid == 0 && pieces > kTokThreads)
+            ptx::cp_async_16_part(mine + j * kRow + kTokThreads * 16, s.piece + kTokThreads * VE,
+                                  min(s.bytes - kTokThreads * 16, 16));
     }
     // the row's single elements meanwhile
-    if (i < cut.head + cut.tail) {
-        const int c = cut.single(i, p.H);
+    if (i0 + tid < cut.head + cut.tail) {
+        const int c = cut.single(i0 + tid, p.H);
         float acc = 0.f;
-        for (int j = 0; j < p.kp; ++j) {
-            const int64_t r = s_row[j];
-            if (r >= 0) acc += s_w[j] * to_f32(src[r * p.H + c]);
-        }
+        for (int j = 0; j < p.kp; ++j)
+            if (s_slot[j].se >= 0) acc += s_w[j] * to_f32(s_slot[j].piece[s_slot[j].se + c - c0]);
         dst[c] = from_f32<T>(acc);
     }
     ptx::cp_async_wait_all();
     __syncthreads();
-    if (static_cast<int>(threadIdx.x) >= n) return;
+    if (tid >= n) return;
     float acc[VE];
 #pragma unroll
     for (int u = 0; u < VE; ++u) acc[u] = 0.f;
     for (int j = 0; j < p.kp; ++j) {
-        const int64_t r = s_row[j];
-        if (r < 0) continue;  // a slot without a row adds nothing
-        const int se = static_cast<int>((r * p.H + c0) & (VE - 1));
-        const uint4 a = ptx::ld_shared_16(mine + j * kRow);
-        const uint4 b = se ? ptx::ld_shared_16(mine + j * kRow + 16) : a;
+        const int se = s_slot[j].se;
+        if (se < 0) continue;  // a slot without a row adds nothing
         Vec<T, VE> v;
         float f[VE];
-        v.w = across<T>(a, b, se);
+        v.w = across<T>(ptx::ld_shared_16(mine + j * kRow), ptx::ld_shared_16(mine + j * kRow + 16), se);
         v.get(f);
 #pragma unroll
         for (int u = 0; u < VE; ++u) acc[u] += s_w[j] * f[u];
     }
     Vec<T, VE> o;
     o.set(acc);
-    o.store(dst + c0 + threadIdx.x * VE);
+    o.store(dst + c0 + tid * VE);
 }
 
 constexpr int kSlotWarps = 8;
