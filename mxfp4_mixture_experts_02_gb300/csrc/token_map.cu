@@ -1,15 +1,19 @@
-// Slots sorted by expert in one launch: the maps of the sort (expert_offsets,
-// a_map, c_map; rows of an expert in ascending slot order) without its virtual
-// experts, for up to 32768 slots.  Longer batches take the sort's three
-// launches, which use more than eight SMs.
+// Slots sorted by expert: the maps of the sort (expert_offsets, a_map, c_map;
+// rows of an expert in ascending slot order) without its virtual experts.
 //
-// One CTA, or a cluster of eight, of 32 warps; a warp owns a run of slots, whose
-// experts stay in registers.  Count: equal experts of 32 slots are found by
-// ballots, the first lane of a group adds its size to the warp's histogram.
-// Then an expert's counts become prefixes over the warps of a CTA, over the
-// CTAs (each reads the others' totals from their shared memory) and over the
+// A CTA has 32 warps; a warp owns a run of slots, whose experts stay in
+// registers.  Count: equal experts of 32 slots are found by ballots, the first
+// lane of a group adds its size to the warp's histogram.  Then an expert's
+// counts become prefixes over the warps of a CTA, over the CTAs and over the
 // experts; and the same walk over the slots gives each its row.  Nothing
 // depends on timing.
+//
+// How the CTAs' counts meet: up to 2048 slots there is one CTA; up to 32768 a
+// cluster of eight reads them from one another's shared memory, in one launch
+// (a call of 32768 slots costs the host 19 us less than the sort's three
+// launches did); up to 1048576 a first launch writes them out and every CTA of
+// a second one, which counts again meanwhile, adds up what it needs.  Longer
+// batches take the sort's own three launches.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -24,26 +28,26 @@ namespace moe {
 namespace {
 
 constexpr int kMapThreads = 1024, kMapWarps = 32, kMapCtas = 8;
-constexpr int kMapRounds = 4;    // of 32 slots: a warp's longest run
-constexpr int kMapAlone = 2048;  // slots that one CTA sorts
+constexpr int kMapAlone = 2048;               // slots that one CTA sorts
+constexpr int kMapCluster = 32768;            // slots that a cluster sorts: four rounds of 32 a warp
+constexpr int kMapRounds = 8, kMapMost = 128;  // rounds and CTAs of the two launches
 
-// ROUNDS * 32 slots per warp at most; p.Et <= 1024.
+// The experts of a warp's run of slots from s0 on, round r in e[r] (-1 past the
+// last slot or without a row here).
 template <int ROUNDS>
-__global__ void __launch_bounds__(kMapThreads, 1) token_map_kernel(SortParams p, int rounds) {
-    extern __shared__ uint16_t s_count[];  // [warps][Et]: a warp's counts, then the rows before its own in the CTA
-    __shared__ int s_total[1024], s_base[1024], s_scan[kMapWarps];
-    cg::cluster_group cluster = cg::this_cluster();
-    const int ctas = static_cast<int>(cluster.num_blocks()), cta = static_cast<int>(cluster.block_rank());
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, n = p.T * p.kp;
-    const int run = rounds * 32, s0 = (cta * kMapWarps + warp) * run;
-    uint16_t* mine = s_count + warp * p.Et;
-
-    int e[ROUNDS];
+__device__ __forceinline__ void load_run(const SortParams& p, int s0, int rounds, int (&e)[ROUNDS]) {
+    const int n = p.T * p.kp;
 #pragma unroll
     for (int r = 0; r < ROUNDS; ++r) {
-        const int s = s0 + 32 * r + lane;
+        const int s = s0 + 32 * r + (threadIdx.x & 31);
         e[r] = r < rounds && s < n ? rs::local_expert(p.ids[s], p) : -1;
     }
+}
+
+// The run's counts in mine[expert].
+template <int ROUNDS>
+__device__ __forceinline__ void count_run(const SortParams& p, int rounds, const int (&e)[ROUNDS], uint16_t* mine) {
+    const int lane = threadIdx.x & 31;
     for (int x = lane; x < p.Et; x += 32) mine[x] = 0;
     __syncwarp();
 #pragma unroll
@@ -53,29 +57,27 @@ __global__ void __launch_bounds__(kMapThreads, 1) token_map_kernel(SortParams p,
         if (e[r] >= 0 && lane == __ffs(peers) - 1) mine[e[r]] += static_cast<uint16_t>(__popc(peers));
         __syncwarp();
     }
-    __syncthreads();
+}
+
+// Thread x: expert x's counts become prefixes over the CTA's warps; the total.
+__device__ __forceinline__ int prefix_warps(const SortParams& p, uint16_t* s_count) {
     int total = 0;
-    if (tid < p.Et) {
+    if (static_cast<int>(threadIdx.x) < p.Et) {
 #pragma unroll 8
         for (int w = 0; w < kMapWarps; ++w) {
-            const int c = s_count[w * p.Et + tid];
-            s_count[w * p.Et + tid] = static_cast<uint16_t>(total);
-            total += c;
-        }
-        s_total[tid] = total;
-    }
-    cluster.sync();
-    int before = 0;  // of this expert in earlier CTAs
-    if (ctas > 1 && tid < p.Et) {
-        total = 0;
-        for (int c = 0; c < ctas; ++c) {
-            const int v = cluster.map_shared_rank(s_total, c)[tid];
-            if (c < cta) before += v;
+            uint16_t& c = s_count[w * p.Et + threadIdx.x];
+            const int v = c;
+            c = static_cast<uint16_t>(total);
             total += v;
         }
     }
-    // prefix over the experts, one per thread
-    int upto = total;
+    return total;
+}
+
+// Thread x: the first row of expert x, from each thread's number of rows.
+__device__ __forceinline__ int first_row(int rows, int* s_scan) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int upto = rows;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int v = __shfl_up_sync(0xffffffffu, upto, o);
@@ -86,15 +88,22 @@ __global__ void __launch_bounds__(kMapThreads, 1) token_map_kernel(SortParams p,
     int earlier = lane < warp ? s_scan[lane] : 0;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) earlier += __shfl_xor_sync(0xffffffffu, earlier, o);
-    upto += earlier;
-    if (tid < p.Et) {
-        s_base[tid] = upto - total + before;
-        if (cta == 0) {
-            p.offsets[tid] = upto - total;
-            if (tid == p.Et - 1) p.offsets[p.Et] = upto;
-        }
-    }
-    cluster.sync();  // s_base is written; and no CTA leaves while another reads its totals
+    return upto + earlier - rows;
+}
+
+// Thread x of one CTA: the offsets.
+__device__ __forceinline__ void write_offsets(const SortParams& p, int first, int rows) {
+    const int x = threadIdx.x;
+    if (x < p.Et) p.offsets[x] = first;
+    if (x == p.Et - 1) p.offsets[p.Et] = first + rows;
+}
+
+// The rows of the run's slots: base[expert] for the CTA, mine[expert] rows of
+// its earlier warps, which advances.
+template <int ROUNDS>
+__device__ __forceinline__ void rank_run(const SortParams& p, int s0, int rounds, const int (&e)[ROUNDS],
+                                         const int* base, uint16_t* mine) {
+    const int lane = threadIdx.x & 31, n = p.T * p.kp;
 #pragma unroll
     for (int r = 0; r < ROUNDS; ++r) {
         if (r >= rounds) break;
@@ -102,7 +111,7 @@ __global__ void __launch_bounds__(kMapThreads, 1) token_map_kernel(SortParams p,
         const uint32_t peers = rs::same_expert_lanes(e[r]);
         int row = -1;
         if (e[r] >= 0) {
-            row = s_base[e[r]] + mine[e[r]] + __popc(peers & ptx::lanemask_lt());
+            row = base[e[r]] + mine[e[r]] + __popc(peers & ptx::lanemask_lt());
             p.a_map[row] = s;
         }
         if (s < n) p.c_map[s] = row;
@@ -112,33 +121,124 @@ __global__ void __launch_bounds__(kMapThreads, 1) token_map_kernel(SortParams p,
     }
 }
 
+// One CTA or one cluster.  p.Et <= 1024.
+template <int ROUNDS>
+__global__ void __launch_bounds__(kMapThreads, 1) token_map_kernel(SortParams p, int rounds) {
+    extern __shared__ uint16_t s_count[];  // [warps][Et]
+    __shared__ int s_total[1024], s_base[1024], s_scan[kMapWarps];
+    cg::cluster_group cluster = cg::this_cluster();
+    const int ctas = static_cast<int>(cluster.num_blocks()), cta = static_cast<int>(cluster.block_rank());
+    const int tid = threadIdx.x, warp = tid >> 5, s0 = (cta * kMapWarps + warp) * rounds * 32;
+    int e[ROUNDS];
+    load_run(p, s0, rounds, e);
+    count_run(p, rounds, e, s_count + warp * p.Et);
+    __syncthreads();
+    int total = prefix_warps(p, s_count);
+    s_total[tid] = total;
+    cluster.sync();
+    int before = 0;  // of this expert in earlier CTAs
+    if (ctas > 1 && tid < p.Et) {
+        total = 0;
+        for (int c = 0; c < ctas; ++c) {
+            const int v = cluster.map_shared_rank(s_total, c)[tid];
+            if (c < cta) before += v;
+            total += v;
+        }
+    }
+    const int first = first_row(total, s_scan);
+    s_base[tid] = first + before;
+    if (cta == 0) write_offsets(p, first, total);
+    cluster.sync();  // s_base is written; and no CTA leaves while another reads its totals
+    rank_run(p, s0, rounds, e, s_base, s_count + warp * p.Et);
+}
+
+// Two launches: each CTA's counts into p.cta_hist [CTA][Et], then the rows.
+template <int ROUNDS>
+__global__ void __launch_bounds__(kMapThreads, 1) map_count_kernel(SortParams p, int rounds) {
+    extern __shared__ uint16_t s_count[];
+    ptx::pdl_launch_dependents();
+    const int warp = threadIdx.x >> 5, s0 = (blockIdx.x * kMapWarps + warp) * rounds * 32;
+    int e[ROUNDS];
+    load_run(p, s0, rounds, e);
+    count_run(p, rounds, e, s_count + warp * p.Et);
+    __syncthreads();
+    const int total = prefix_warps(p, s_count);
+    if (static_cast<int>(threadIdx.x) < p.Et) p.cta_hist[static_cast<size_t>(blockIdx.x) * p.Et + threadIdx.x] = total;
+}
+
+template <int ROUNDS>
+__global__ void __launch_bounds__(kMapThreads, 1) map_rank_kernel(SortParams p, int rounds) {
+    extern __shared__ uint16_t s_count[];
+    __shared__ int s_base[1024], s_scan[kMapWarps];
+    const int tid = threadIdx.x, warp = tid >> 5, s0 = (blockIdx.x * kMapWarps + warp) * rounds * 32;
+    // the ids are older than the first launch, which started after them
+    int e[ROUNDS];
+    load_run(p, s0, rounds, e);
+    count_run(p, rounds, e, s_count + warp * p.Et);
+    __syncthreads();
+    prefix_warps(p, s_count);
+    ptx::pdl_wait();
+    int before = 0, total = 0;
+    if (tid < p.Et) {
+        const int ctas = gridDim.x, cta = blockIdx.x;
+        const int* h = p.cta_hist + tid;
+        for (int c0 = 0; c0 < ctas; c0 += 16) {
+            int v[16];
+#pragma unroll
+            for (int u = 0; u < 16; ++u) v[u] = c0 + u < ctas ? h[static_cast<size_t>(c0 + u) * p.Et] : 0;
+#pragma unroll
+            for (int u = 0; u < 16; ++u) {
+                if (c0 + u < cta) before += v[u];
+                total += v[u];
+            }
+        }
+    }
+    const int first = first_row(total, s_scan);
+    s_base[tid] = first + before;
+    if (blockIdx.x == 0) write_offsets(p, first, total);
+    __syncthreads();
+    rank_run(p, s0, rounds, e, s_base, s_count + warp * p.Et);
+}
+
+template <typename K>
+cudaError_t launch_map(K kernel, int ctas, int cluster, bool pdl, const SortParams& p, int rounds, cudaStream_t st) {
+    const size_t smem = static_cast<size_t>(kMapWarps) * p.Et * sizeof(uint16_t);  // at most 64 KB
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    if (!cluster) return launch_kernel(kernel, dim3(ctas), dim3(kMapThreads), smem, st, pdl, p, rounds);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(kMapThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = cluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, p, rounds);
+}
+
 }  // namespace
 
 cudaError_t launch_token_map(const SortParams& p, cudaStream_t st) {
     const int n = p.T * p.kp;
-    if (n > kMapCtas * kMapWarps * kMapRounds * 32) return launch_sort(p, st, false);
-    const int ctas = n <= kMapAlone ? 1 : kMapCtas;
-    const int rounds = std::max(1, (n + ctas * kMapWarps * 32 - 1) / (ctas * kMapWarps * 32));
-    const size_t smem = static_cast<size_t>(kMapWarps) * p.Et * sizeof(uint16_t);  // at most 64 KB
-    auto go = [&](auto kernel) {
-        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             static_cast<int>(smem));
-        if (e != cudaSuccess) return e;
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(ctas);
-        cfg.blockDim = dim3(kMapThreads);
-        cfg.dynamicSmemBytes = smem;
-        cfg.stream = st;
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = ctas;
-        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        return cudaLaunchKernelEx(&cfg, kernel, p, rounds);
-    };
-    if (rounds <= 2) return go(token_map_kernel<2>);
-    return go(token_map_kernel<kMapRounds>);
+    constexpr int kRound = kMapWarps * 32;  // slots of a CTA's round
+    if (n <= kMapCluster) {
+        const int ctas = n <= kMapAlone ? 1 : kMapCtas;
+        const int rounds = std::max(1, (n + ctas * kRound - 1) / (ctas * kRound));
+        if (rounds <= 2) return launch_map(token_map_kernel<2>, ctas, ctas, false, p, rounds, st);
+        return launch_map(token_map_kernel<4>, ctas, ctas, false, p, rounds, st);
+    }
+    if (n > kMapMost * kMapRounds * kRound) return launch_sort(p, st, false);
+    // rounds enough that no more than 64 CTAs' counts are added up, where eight allow it
+    const int rounds = std::clamp((n + 64 * kRound - 1) / (64 * kRound), 4, kMapRounds);
+    const int ctas = (n + rounds * kRound - 1) / (rounds * kRound);
+    const cudaError_t e = launch_map(map_count_kernel<kMapRounds>, ctas, 0, false, p, rounds, st);
+    if (e != cudaSuccess) return e;
+    return launch_map(map_rank_kernel<kMapRounds>, ctas, 0, true, p, rounds, st);
 }
 
 }  // namespace moe

@@ -284,6 +284,24 @@ def test_token_map_long_batch_and_given_buffers():
     assert maps.a_map[:len(a)].tolist() == a and (maps.a_map[len(a):] == -7).all()
 
 
+@pytest.mark.parametrize("T", [1, 127, 128, 129, 2047, 2048, 2049, 20000, 65536, 65537])
+@pytest.mark.parametrize("E,local", [(32, 32), (1024, 512)])
+def test_token_map_on_either_side_of_each_way_of_sorting(T, E, local):
+    # 16 slots a token: 2048, 32768 and 1048576 slots are where the launches change
+    g = gen(T)
+    shape = moe.MoeTokenShape(T, E, local, E - local, 16, 0, 8)
+    ids = torch.randint(0, E, (T, 16), generator=g, device="cuda", dtype=torch.int32)
+    maps = moe.moe_token_map(shape, ids)
+    e = ids.view(-1).long() - (E - local)
+    e = torch.where(e >= 0, e, local)
+    by, order = torch.sort(e, stable=True)
+    R = int((by < local).sum())
+    c = torch.full_like(order, -1)
+    c[order[:R]] = torch.arange(R, device="cuda")
+    assert torch.equal(maps.a_map[:R].long(), order[:R]) and torch.equal(maps.c_map.view(-1).long(), c)
+    assert torch.equal(maps.expert_offsets.long(), torch.searchsorted(by, torch.arange(local + 1, device="cuda")))
+
+
 def gather(rows, c):
     """[T, k', H] in 64 bits, zero without a row."""
     return torch.where((c >= 0)[:, :, None], rows[c.clamp_min(0).long()].double(), 0.0)
