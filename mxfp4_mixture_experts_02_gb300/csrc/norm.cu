@@ -13,9 +13,13 @@
 // Rows off the 16-byte grid: rows 8 apart start at the same place between grid
 // points, so a CTA takes rows 8 n apart, and its threads keep the same pieces
 // of the grid, which reach over the ends of the row.
+#include <cooperative_groups.h>
+
 #include <algorithm>
 
 #include "train.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace moe {
 
@@ -134,6 +138,7 @@ __device__ __forceinline__ void params(float* to, const void* p, bool f32, int c
 __device__ __forceinline__ float half_of(float2 v, int second) { return second ? v.y : v.x; }
 
 constexpr int kGroupThreads = 128;  // CTA of a kernel whose rows take a group of lanes
+constexpr int kNormCluster = 8;     // CTAs of the gradient for few rows
 constexpr int kRowThreads = 512;    // largest CTA of a kernel whose rows take the CTA
 
 // Resident CTAs of C threads by the columns of a thread: with up to eight, 64
@@ -158,7 +163,7 @@ __global__ void __launch_bounds__(C, ctas_for(V * kVe<T, LIE>, C, GROUP))
     // rows of this thread's group or CTA that are still to be fetched, and
     // rounds of the CTA
     int left = row < rows ? (rows - row - 1) / hop + 1 : 0;
-    int rounds = (rows - row0 - 1) / hop + 1;
+    int rounds = row0 < rows ? (rows - row0 - 1) / hop + 1 : 0;
     // columns of this thread's first access that belong to the row before
     const int se = LIE == kOff ? (row % VE) * (p.cols % VE) % VE : 0;
     const char *x = static_cast<const char*>(p.x), *res = static_cast<const char*>(p.residual);
@@ -357,7 +362,9 @@ __global__ void __launch_bounds__(1024) norm_long_kernel(NormParams p) {
 //   dx = rstd (a - mean(a) - xh mean(a xh)) (+ dh, the residual stream's)
 //   dw = sum over rows of dy xh,  db = sum over rows of dy
 // A thread's column sums leave once, as one row of partial sums per CTA; a
-// second launch adds those in a fixed order.
+// second launch adds those in a fixed order.  For few rows there is one cluster
+// of eight CTAs, which adds its sums itself: 32 rows take one launch instead of
+// two.
 template <typename T, int LIE, int V, int S, int C, bool GROUP>
 __global__ void __launch_bounds__(C, ctas_for(V * kVe<T, LIE>, C, GROUP))
     norm_grad_kernel(NormGradParams p, int L) {
@@ -375,7 +382,7 @@ __global__ void __launch_bounds__(C, ctas_for(V * kVe<T, LIE>, C, GROUP))
     // rows of this thread's group or CTA that are still to be fetched, and
     // rounds of the CTA
     int left = row < rows ? (rows - row - 1) / hop + 1 : 0;
-    int rounds = (rows - row0 - 1) / hop + 1;
+    int rounds = row0 < rows ? (rows - row0 - 1) / hop + 1 : 0;
     // columns of this thread's first access that belong to the row before
     const int se = LIE == kOff ? (row % VE) * (p.cols % VE) % VE : 0;
     const char *h = static_cast<const char*>(p.h), *dy = static_cast<const char*>(p.dy);
@@ -509,8 +516,15 @@ __global__ void __launch_bounds__(C, ctas_for(V * kVe<T, LIE>, C, GROUP))
         st = R::next(st);
         ahead = R::next(ahead);
     }
-    if (!p.partial) return;
-    float* part = p.partial + static_cast<int64_t>(blockIdx.x) * 2 * p.cols;
+    if (!p.dweight && !p.dbias) return;
+    // The CTA's sums: straight to its row of partial sums, or into shared
+    // memory (the ring is free: no row is on its way), where a group's lanes
+    // or a cluster's CTAs join theirs.
+    const bool few = !p.partial;
+    float* s_sum = reinterpret_cast<float*>(s_ring);
+    float* part = few ? s_sum : p.partial + static_cast<int64_t>(blockIdx.x) * 2 * p.cols;
+    ptx::cp_async_wait<0>();
+    if (GROUP || few) __syncthreads();
     if (!GROUP) {
 #pragma unroll
         for (int i = 0; i < V; ++i)
@@ -525,8 +539,6 @@ __global__ void __launch_bounds__(C, ctas_for(V * kVe<T, LIE>, C, GROUP))
     } else {
         // the warp's groups by shuffles, then the warps one after another; off
         // the grid the groups hold different columns, so all one after another
-        // (the ring is free: no row is on its way)
-        float* s_sum = reinterpret_cast<float*>(s_ring);
         constexpr bool kOne = LIE == kOff;
         if (!kOne) {
 #pragma unroll
@@ -538,10 +550,8 @@ __global__ void __launch_bounds__(C, ctas_for(V * kVe<T, LIE>, C, GROUP))
                     ab[k].y += __shfl_xor_sync(0xffffffffu, ab[k].y, o);
                 }
         }
-        ptx::cp_async_wait<0>();
         const int turns = kOne ? C / L : C / 32, my_turn = kOne ? threadIdx.x / L : threadIdx.x >> 5;
         for (int t = 0; t < turns; ++t) {
-            __syncthreads();
             if (my_turn == t && (kOne || wl < L)) {
 #pragma unroll
                 for (int i = 0; i < V; ++i)
@@ -555,9 +565,23 @@ __global__ void __launch_bounds__(C, ctas_for(V * kVe<T, LIE>, C, GROUP))
                         }
                     }
             }
+            __syncthreads();
         }
-        __syncthreads();
-        for (int c = threadIdx.x; c < 2 * p.cols; c += kGroupThreads) part[c] = s_sum[c];
+        if (!few)
+            for (int c = threadIdx.x; c < 2 * p.cols; c += C) part[c] = s_sum[c];
+    }
+    if (few) {
+        cg::cluster_group cluster = cg::this_cluster();
+        cluster.sync();
+        for (int c = blockIdx.x * blockDim.x + threadIdx.x; c < 2 * p.cols; c += gridDim.x * blockDim.x) {
+            float t = 0.f;
+#pragma unroll
+            for (int k = 0; k < kNormCluster; ++k) t += cluster.map_shared_rank(s_sum, k)[c];
+            float* to = c < p.cols ? p.dweight : p.dbias;
+            if (to) to[c < p.cols ? c : c - p.cols] = t;
+        }
+        cluster.sync();  // no CTA leaves while another reads its sums
+        return;
     }
     ptx::pdl_launch_dependents();
 }
@@ -717,6 +741,30 @@ cudaError_t launch_rows(K kernel, const P& p, int L, int ctas_per_sm, int max_ct
 template <typename T, int LIE>
 constexpr int kLong = LIE == kGrid ? kFull<T> : 1;
 
+// The gradient of few rows in one cluster.
+template <typename R, typename K>
+cudaError_t launch_few(K kernel, const NormGradParams& p, int threads, int L, cudaStream_t st) {
+    // the column sums take the ring's place
+    const size_t smem = std::max<size_t>(R::kEnd, size_t(2) * p.cols * sizeof(float));
+    if (smem > 46 << 10) {
+        const cudaError_t e =
+            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        if (e != cudaSuccess) return e;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(kNormCluster);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = kNormCluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, p, L);
+}
+
 template <typename T, int LIE>
 cudaError_t launch_norm_t(const NormParams& p, cudaStream_t st) {
     constexpr int VE = kVe<T, LIE>;
@@ -734,6 +782,7 @@ template <typename T, int LIE>
 cudaError_t launch_norm_grad_t(const NormGradParams& p, cudaStream_t st) {
     constexpr int VE = kVe<T, LIE>;
     int parts = 0;
+    bool alone = false;
     cudaError_t e = cudaSuccess;
     if (p.rows > 0)  // without rows the sums are zero
         e = by_row<VE, VE == 1 ? 1 : 2, VE == 1 ? 4 : 2, 16>(accesses<T, LIE>(p.cols), [&](auto v, auto c, auto group, int L) {
@@ -750,12 +799,22 @@ cudaError_t launch_norm_grad_t(const NormGradParams& p, cudaStream_t st) {
                 return launch_kernel(norm_grad_long_kernel<T, VL>, dim3(static_cast<unsigned>(p.rows)), dim3(1024), 0,
                                      st, false, p);
             } else {
-                return launch_rows<Ring<T, LIE, V, S, 3, C, group.value>, C, group.value>(
-                    norm_grad_kernel<T, LIE, V, S, C, group.value>, p, L, ctas_for(V * VE, C, group.value), kNormMaxPartials, &parts,
-                    st);
+                using R = Ring<T, LIE, V, S, 3, C, group.value>;
+                const auto kernel = norm_grad_kernel<T, LIE, V, S, C, group.value>;
+                // few rows: four for each group or CTA of a cluster, whose sums
+                // fit the ring (single 16-bit elements have none)
+                const int per = group.value ? C / L : 1;
+                if (R::kAsync && p.partial && p.rows <= 4 * kNormCluster * per) {
+                    NormGradParams q = p;
+                    q.partial = nullptr;
+                    alone = true;
+                    return launch_few<R>(kernel, q, group.value ? C : L, L, st);
+                }
+                return launch_rows<R, C, group.value>(kernel, p, L, ctas_for(V * VE, C, group.value), kNormMaxPartials,
+                                                      &parts, st);
             }
         });
-    if (e != cudaSuccess || !p.partial) return e;
+    if (e != cudaSuccess || !p.partial || alone) return e;
     return launch_kernel(norm_grad_sum_kernel, dim3((2 * p.cols + 31) / 32), dim3(1024), 0, st, true, p, parts);
 }
 
