@@ -371,6 +371,7 @@ __global__ void __launch_bounds__(C, ctas_for(V * kVe<T, LIE>, C, GROUP))
     extern __shared__ uint4 s_ring[];
     static_assert(kRowThreads == 16 * 32, "half a warp holds the warps' sums");
     __shared__ float s_part[2][2][16];
+    ptx::pdl_launch_dependents();  // the launch that adds the sums waits for this one's end itself
     using R = Ring<T, LIE, V, S, 3, C, GROUP>;
     constexpr int VE = R::VE;
     const R ring(s_ring);
@@ -517,25 +518,41 @@ __global__ void __launch_bounds__(C, ctas_for(V * kVe<T, LIE>, C, GROUP))
         ahead = R::next(ahead);
     }
     if (!p.dweight && !p.dbias) return;
-    // The CTA's sums: straight to its row of partial sums, or into shared
-    // memory (the ring is free: no row is on its way), where a group's lanes
-    // or a cluster's CTAs join theirs.
+    // The CTA's sums go to its row of partial sums: whole accesses on the grid,
+    // else by way of shared memory (the ring is free: no row is on its way),
+    // where a group's lanes or a cluster's CTAs join theirs as well.  (Floats
+    // stored one by one, eight apart from lane to lane, took 10 of 18 us of a
+    // gradient of 1000 x 3584.)
     const bool few = !p.partial;
+    const bool staged = GROUP || few || LIE == kOff;
     float* s_sum = reinterpret_cast<float*>(s_ring);
-    float* part = few ? s_sum : p.partial + static_cast<int64_t>(blockIdx.x) * 2 * p.cols;
+    float* part = p.partial + static_cast<int64_t>(blockIdx.x) * 2 * p.cols;
     ptx::cp_async_wait<0>();
-    if (GROUP || few) __syncthreads();
+    if (staged) __syncthreads();
     if (!GROUP) {
+        float* to = staged ? s_sum : part;
 #pragma unroll
         for (int i = 0; i < V; ++i)
             if (has(i)) {
+                if (LIE == kGrid && !staged) {
+#pragma unroll
+                    for (int u = 0; u < VE; u += 4) {
+                        const int k = (i * VE + u) / 2;
+                        *reinterpret_cast<float4*>(to + col(i) + u) =
+                            make_float4(aw[k].x, aw[k].y, aw[k + 1].x, aw[k + 1].y);
+                        *reinterpret_cast<float4*>(to + p.cols + col(i) + u) =
+                            make_float4(ab[k].x, ab[k].y, ab[k + 1].x, ab[k + 1].y);
+                    }
+                    continue;
+                }
 #pragma unroll
                 for (int u = 0; u < VE; ++u) {
                     if (LIE == kOff && (col(i) + u < 0 || col(i) + u >= p.cols)) continue;
-                    part[col(i) + u] = half_of(aw[(i * VE + u) / 2], (i * VE + u) & 1);
-                    part[p.cols + col(i) + u] = half_of(ab[(i * VE + u) / 2], (i * VE + u) & 1);
+                    to[col(i) + u] = half_of(aw[(i * VE + u) / 2], (i * VE + u) & 1);
+                    to[p.cols + col(i) + u] = half_of(ab[(i * VE + u) / 2], (i * VE + u) & 1);
                 }
             }
+        if (staged) __syncthreads();
     } else {
         // the warp's groups by shuffles, then the warps one after another; off
         // the grid the groups hold different columns, so all one after another
@@ -567,9 +584,9 @@ __global__ void __launch_bounds__(C, ctas_for(V * kVe<T, LIE>, C, GROUP))
             }
             __syncthreads();
         }
-        if (!few)
-            for (int c = threadIdx.x; c < 2 * p.cols; c += C) part[c] = s_sum[c];
     }
+    if (staged && !few)
+        for (int c = threadIdx.x; c < 2 * p.cols; c += blockDim.x) part[c] = s_sum[c];
     if (few) {
         cg::cluster_group cluster = cg::this_cluster();
         cluster.sync();
@@ -581,9 +598,7 @@ __global__ void __launch_bounds__(C, ctas_for(V * kVe<T, LIE>, C, GROUP))
             if (to) to[c < p.cols ? c : c - p.cols] = t;
         }
         cluster.sync();  // no CTA leaves while another reads its sums
-        return;
     }
-    ptx::pdl_launch_dependents();
 }
 
 // Long rows: dx alone, the row re-read from the caches.
@@ -656,6 +671,8 @@ __global__ void __launch_bounds__(256) norm_grad_cols_kernel(NormGradParams p) {
     for (int u = 0; u < VE; ++u) part[u] = aw[u], part[p.cols + u] = ab[u];
 }
 
+constexpr int kSumBatch = 10;  // loads in flight: two batches for all partial rows
+
 // Column sums over the partial rows: 32 columns per CTA, 32 threads deep.
 __global__ void __launch_bounds__(1024) norm_grad_sum_kernel(NormGradParams p, int parts) {
     __shared__ float s[32][33];
@@ -663,7 +680,14 @@ __global__ void __launch_bounds__(1024) norm_grad_sum_kernel(NormGradParams p, i
     const int c = blockIdx.x * 32 + (threadIdx.x & 31), depth = threadIdx.x >> 5;
     float a = 0.f;
     if (c < 2 * p.cols)
-        for (int g = depth; g < parts; g += 32) a += p.partial[static_cast<int64_t>(g) * 2 * p.cols + c];
+        for (int g0 = depth; g0 < parts; g0 += 32 * kSumBatch) {
+            float v[kSumBatch];
+#pragma unroll
+            for (int u = 0; u < kSumBatch; ++u)
+                v[u] = g0 + 32 * u < parts ? p.partial[static_cast<int64_t>(g0 + 32 * u) * 2 * p.cols + c] : 0.f;
+#pragma unroll
+            for (int u = 0; u < kSumBatch; ++u) a += v[u];
+        }
     s[depth][threadIdx.x & 31] = a;
     __syncthreads();
     const float t = lanes_sum(s[threadIdx.x & 31][depth], 32);  // column `depth` of this CTA's 32
@@ -720,6 +744,8 @@ constexpr int stages_for(int bytes) { return bytes <= 32 ? 3 : 2; }
 // and the ring.
 template <typename R, int C, bool GROUP, typename P, typename K>
 cudaError_t launch_rows(K kernel, const P& p, int L, int ctas_per_sm, int max_ctas, int* ctas_out, cudaStream_t st) {
+    // the gradient's column sums (two floats a column) take the ring's place:
+    // a thread's slots hold more than those of its columns
     constexpr int kSmem = R::kEnd;
     static_assert(kSmem <= 224 << 10, "more than an SM has");
     const int threads = GROUP ? C : L;
