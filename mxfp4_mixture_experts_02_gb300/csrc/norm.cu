@@ -70,8 +70,11 @@ struct Ring {
     // (the tensor may end there) and become zero.
     __device__ __forceinline__ void fetch(uint32_t st, int t, int i, const char* src, int c, int cols) const {
         const uint32_t to = mine + st + t * kTensor + i * kAccess;
+        // through L1, but for the gradient of fp32 rows: 131072 x 201 take 83 us
+        // past it and 100 through it, 27894 x 3585 bf16 147 and 138
         if constexpr (LIE == kOff)
-            ptx::cp_async_16_part(to, src, min((cols - c) * static_cast<int>(sizeof(T)), 16));
+            ptx::cp_async_16_part<N == 2 || sizeof(T) == 2>(to, src,
+                                                            min((cols - c) * static_cast<int>(sizeof(T)), 16));
         else if constexpr (kBytes == 16) ptx::cp_async_16(to, src);
         else if constexpr (kAsync) ptx::cp_async_4(to, src);
     }
@@ -836,8 +839,11 @@ cudaError_t launch_norm_grad_t(const NormGradParams& p, cudaStream_t st) {
                     alone = true;
                     return launch_few<R>(kernel, q, group.value ? C : L, L, st);
                 }
-                return launch_rows<R, C, group.value>(kernel, p, L, ctas_for(V * VE, C, group.value), kNormMaxPartials,
-                                                      &parts, st);
+                // each CTA's sums cost about as much as four rows: where there
+                // are rows for it, it takes four rounds
+                const int64_t most = std::clamp<int64_t>((p.rows + 4 * per - 1) / (4 * per), kSms, kNormMaxPartials);
+                return launch_rows<R, C, group.value>(kernel, p, L, ctas_for(V * VE, C, group.value),
+                                                      static_cast<int>((most + 7) / 8 * 8), &parts, st);
             }
         });
     if (e != cudaSuccess || !p.partial || alone) return e;

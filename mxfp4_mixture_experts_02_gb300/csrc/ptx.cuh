@@ -194,9 +194,13 @@ __device__ __forceinline__ uint32_t ld_global_u8(const void* p) {
 }
 
 // 16 bytes of shared memory from `bytes` <= 16 of global memory and zeros (the
-// rest is not read).  Cached in L1: the neighbouring thread reads the same.
+// rest is not read), through L1 or past it.
+template <bool L1>
 __device__ __forceinline__ void cp_async_16_part(uint32_t dst, const void* src, uint32_t bytes) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+    if (L1)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+    else
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ uint4 ld_shared_16(uint32_t at) {
     uint4 v;

@@ -207,10 +207,10 @@ __global__ void __launch_bounds__(kTokThreads) unpermute_off_kernel(TokenParams 
         const Slot s = s_slot[j];
         const int pieces = n + (s.se > 0);
         if (s.se < 0 || tid >= pieces) continue;
-        ptx::cp_async_16_part(mine + j * kRow, s.piece + tid * VE, min(s.bytes - tid * 16, 16));
+        ptx::cp_async_16_part<false>(mine + j * kRow, s.piece + tid * VE, min(s.bytes - tid * 16, 16));
         if (tid == 0 && pieces > kTokThreads)
-            ptx::cp_async_16_part(mine + j * kRow + kTokThreads * 16, s.piece + kTokThreads * VE,
-                                  min(s.bytes - kTokThreads * 16, 16));
+            ptx::cp_async_16_part<false>(mine + j * kRow + kTokThreads * 16, s.piece + kTokThreads * VE,
+                                         min(s.bytes - kTokThreads * 16, 16));
     }
     // the row's single elements meanwhile
     if (i0 + tid < cut.head + cut.tail) {
