@@ -438,7 +438,7 @@ int moe_test_set_stall(uint64_t stall_ns);
  * except that sums over rows are written as zero. */
 enum { MOE_DTYPE_BF16 = 0, MOE_DTYPE_F16 = 1, MOE_DTYPE_F32 = 2 };
 
-/* rows [0, 2^31), cols [1, 2^20]; dtype of the rows, w_dtype of weight and
+/* rows [0, 2^30], cols [1, 2^20]; dtype of the rows, w_dtype of weight and
  * bias (MOE_DTYPE_F32 or the rows'); eps >= 0 and finite. */
 typedef struct moe_norm_shape {
     int64_t rows;

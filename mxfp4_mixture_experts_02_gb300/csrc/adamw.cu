@@ -5,6 +5,12 @@
 // m and v are rounded operation by operation, as the formulas are written, so
 // the states follow from them alone.
 //
+// With fp32 states the bytes bind: 128 M parameters and bf16 gradients (26
+// bytes each) take 504 us, 6.6 TB/s.  With MXFP8 states (14.1 bytes) the update
+// binds, about 60 instructions an element of which the 64-bit random numbers
+// are 10 and the two codes 14: 96 M take 256 us, 5.3 TB/s, and fp32 gradients
+// hardly more.
+//
 // 8-bit states: m and sqrt(v) as E4M3 codes with one power-of-two scale per
 // 32 values, 2^e with e = floor(log2 max) - 7 (the largest magnitude lies in
 // [128, 256), so nothing saturates).  The square root halves the exponent

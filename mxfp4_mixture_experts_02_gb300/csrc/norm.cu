@@ -10,9 +10,18 @@
 // their way meanwhile: each thread copies its own columns into its own slots
 // of a ring in shared memory, which needs no barrier and no registers.
 //
+// Measured at 32768 x 3584 bf16 (940 MB; a plain copy runs at 6.5 TB/s there):
+// forward with a residual 148 us, 6.3 TB/s, with one more row on its way (two
+// more: 160 us, three: 166); gradient with a residual 142 us, 6.6 TB/s, with
+// two accesses a thread, two CTAs of 224 threads an SM and two more rows on
+// their way (one access and 448 threads: 158 us).  A CTA per row without the
+// ring took 157 us forward.
+//
 // Rows off the 16-byte grid: rows 8 apart start at the same place between grid
 // points, so a CTA takes rows 8 n apart, and its threads keep the same pieces
-// of the grid, which reach over the ends of the row.
+// of the grid, which reach over the ends of the row.  27894 x 3585 bf16 take 139
+// us forward (5.7 TB/s); element by element they took 467, and with the columns
+// put together from two pieces each 324.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -676,7 +685,8 @@ __global__ void __launch_bounds__(256) norm_grad_cols_kernel(NormGradParams p) {
 
 constexpr int kSumBatch = 10;  // loads in flight: two batches for all partial rows
 
-// Column sums over the partial rows: 32 columns per CTA, 32 threads deep.
+// Column sums over the partial rows, mostly from L2: 32 columns per CTA, 32
+// threads deep.  About 4 us for 304 rows of 2 x 3584.
 __global__ void __launch_bounds__(1024) norm_grad_sum_kernel(NormGradParams p, int parts) {
     __shared__ float s[32][33];
     ptx::pdl_wait();
@@ -740,7 +750,8 @@ cudaError_t by_row(int nvec, F f) {
 }
 
 // Stages of the gradient by the bytes of a thread and row: 64 bytes of three
-// tensors in 512 threads leave room for two.
+// tensors in 512 threads leave room for two.  (Two stages of the smaller ones
+// took 153 us instead of 148 at 32768 x 3584, four 153.)
 constexpr int stages_for(int bytes) { return bytes <= 32 ? 3 : 2; }
 
 // One launch over all rows, as many CTAs as are resident by the launch bounds

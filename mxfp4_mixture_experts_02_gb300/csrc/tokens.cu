@@ -8,7 +8,10 @@
 //                      dw[t, j] = <dout[t], rows[c_map[t, j]]>, 0 at -1
 // (the shapes of "[SGLang] CUTLASS MoE", sections 2 and 5, in the rows' own
 // type).  Sums are in 32 bits, j ascending.  All are bound by the rows they
-// read and write: a token's row is read once, each expert row once.
+// read and write: a token's row is read once, each expert row once.  Measured
+// with hidden 3584 bf16: 131072 rows written by permute in 151 us (6.2 TB/s),
+// 524288 rows summed into 32768 tokens in 568 us (7.0 TB/s), both gradients of
+// 4096 x 17 slots in 153 us (6.7 TB/s).
 //
 // Rows off the 16-byte grid: a thread takes a whole piece of the grid in the row
 // that is written and puts the other side's columns together from the two
@@ -135,7 +138,9 @@ __global__ void __launch_bounds__(kTokThreads) permute_kernel(TokenParams p) {
     }
 }
 
-constexpr int kRowBatch = 4;  // rows in flight per thread
+// Rows in flight per thread.  Eight cost resident CTAs: 8189 tokens with half
+// of their 17 slots here take 100 us instead of 92.
+constexpr int kRowBatch = 4;
 
 template <typename T, int LIE>
 __global__ void __launch_bounds__(kTokThreads) unpermute_kernel(TokenParams p) {
@@ -173,7 +178,9 @@ __global__ void __launch_bounds__(kTokThreads) unpermute_kernel(TokenParams p) {
 
 // Off the grid: the pieces that a chunk's rows lie in come into shared memory
 // on their own, all slots' at once, and each thread puts its columns of a row
-// together from two of them.
+// together from two of them.  65536 rows of 3585 bf16 take 106 us (5.0 TB/s;
+// with both pieces loaded to registers, four rows in flight, 174); what is left
+// is the instructions that put the columns together.
 template <typename T>
 __global__ void __launch_bounds__(kTokThreads) unpermute_off_kernel(TokenParams p) {
     constexpr int VE = kFull<T>;
@@ -245,7 +252,9 @@ constexpr int kSlotWarps = 8;
 
 // A warp per slot: it walks over the row once, so the routing weight's gradient
 // (a sum over the whole row) needs one reduction and no barrier; the token's
-// row comes from L1 for all its slots but the first.
+// row comes from L1 for all its slots but the first.  A CTA per token, with a
+// reduction for each slot and chunk, took 165 us instead of 153 for 4096 x 17
+// slots of 3584 and 221 instead of 124 for 262144 slots of 512.
 template <typename T, int LIE>
 __global__ void __launch_bounds__(kSlotWarps * 32) unpermute_grad_kernel(TokenParams p) {
     constexpr int VE = kVe<T, LIE>;

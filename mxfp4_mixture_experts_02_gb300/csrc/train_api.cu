@@ -34,7 +34,7 @@ int check_norm(const moe_norm_shape* s) {
     if (!s) return MOE_ERR_NULL;
     const int b = elem_bytes(s->dtype);
     if (!b || (s->w_dtype != MOE_DTYPE_F32 && s->w_dtype != s->dtype)) return MOE_ERR_SHAPE;
-    if (s->rows < 0 || s->rows > 0x7FFFFFFF || s->cols < 1 || s->cols > (1 << 20)) return MOE_ERR_SHAPE;
+    if (s->rows < 0 || s->rows > (1 << 30) || s->cols < 1 || s->cols > (1 << 20)) return MOE_ERR_SHAPE;
     if (!(s->eps >= 0.f) || !(s->eps <= 3.0e38f)) return MOE_ERR_SHAPE;
     return MOE_OK;
 }

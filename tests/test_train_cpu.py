@@ -21,7 +21,7 @@ def tokens(**kw):
 
 
 BAD_NORM = [dict(dtype=3), dict(dtype=-1), dict(w_dtype=1), dict(dtype=2, w_dtype=0), dict(rows=-1), dict(cols=0),
-            dict(rows=1 << 31), dict(cols=(1 << 20) + 1), dict(eps=-1.0), dict(eps=float("nan")),
+            dict(rows=(1 << 30) + 1), dict(cols=(1 << 20) + 1), dict(eps=-1.0), dict(eps=float("nan")),
             dict(eps=float("inf"))]
 BAD_TOKENS = [dict(dtype=3), dict(hidden=0), dict(hidden=(1 << 20) + 1), dict(top_k=0), dict(top_k=9), dict(T=-1),
               dict(top_k=33, E_global=64), dict(E_global=1025), dict(num_shared=2),
