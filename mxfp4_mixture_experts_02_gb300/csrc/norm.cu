@@ -310,6 +310,99 @@ __global__ void __launch_bounds__(C, ctas_for(V * kVe<T, LIE>, C, GROUP))
     }
 }
 
+// A piece of a row on the 16-byte grid, from column c on; columns outside the
+// row are zero.  more: a row comes after it, so the piece ends in the tensor.
+template <typename T, int LIE>
+__device__ __forceinline__ Vec<T, kFull<T>> piece(const T* p, int c, int cols, bool more) {
+    constexpr int VE = kFull<T>;
+    Vec<T, VE> v;
+    if (whole<T, LIE>(c, cols)) {
+        v.load(p);
+        return v;
+    }
+    float f[VE];
+    if (LIE == kOff && (more || c + VE <= cols)) {
+        v.load(p);
+        v.get(f);
+    } else {
+#pragma unroll
+        for (int u = 0; u < VE; ++u) f[u] = c + u >= 0 && c + u < cols ? to_f32(p[u]) : 0.f;
+    }
+#pragma unroll
+    for (int u = 0; u < VE; ++u)
+        if (c + u < 0 || c + u >= cols) f[u] = 0.f;
+    v.set(f);
+    return v;
+}
+
+// Rows of more columns than the ring's threads hold: a CTA per row, which stays
+// in registers in its own type; weights come from the caches.
+template <typename T, int LIE, int V>
+__global__ void __launch_bounds__(1024, 1) norm_wide_kernel(NormParams p) {
+    __shared__ float s_part[2][32];
+    constexpr int VE = kFull<T>;
+    const int64_t base = static_cast<int64_t>(blockIdx.x) * p.cols;
+    const bool more = blockIdx.x + 1 < p.rows;
+    const int n = blockDim.x, first = static_cast<int>(threadIdx.x) * VE - before<T, LIE>(base);
+    auto col = [&](int i) { return i * n * VE + first; };
+    const T *x = static_cast<const T*>(p.x) + base, *r = static_cast<const T*>(p.residual) + base;
+    Vec<T, VE> h[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        h[i].w = make_uint4(0, 0, 0, 0);
+        if (col(i) < p.cols) h[i] = piece<T, LIE>(x + col(i), col(i), p.cols, more);
+    }
+    float f[VE], g[VE], s = 0.f, q = 0.f;
+    if (p.residual) {
+        Vec<T, VE> e[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (col(i) < p.cols) e[i] = piece<T, LIE>(r + col(i), col(i), p.cols, more);
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (col(i) < p.cols) {
+                h[i].get(f);
+                e[i].get(g);
+#pragma unroll
+                for (int u = 0; u < VE; ++u) f[u] += g[u];
+                h[i].set(f);  // as it is stored
+                put<T, LIE>(f, reinterpret_cast<char*>(static_cast<T*>(p.h) + base + col(i)), col(i), p.cols);
+            }
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        h[i].get(f);
+#pragma unroll
+        for (int u = 0; u < VE; ++u) s += f[u];
+    }
+    const float inv_n = 1.0f / static_cast<float>(p.cols);
+    const float mean = block_sum(s, s_part[0]) * inv_n;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        h[i].get(f);
+#pragma unroll
+        for (int u = 0; u < VE; ++u)
+            if (LIE == kOff ? col(i) + u >= 0 && col(i) + u < p.cols : col(i) < p.cols)
+                q += (f[u] - mean) * (f[u] - mean);
+    }
+    const float rstd = 1.0f / sqrtf(block_sum(q, s_part[1]) * inv_n + p.eps);
+    if (threadIdx.x == 0) {
+        p.mean[blockIdx.x] = mean;
+        p.rstd[blockIdx.x] = rstd;
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        if (col(i) < p.cols) {
+            float w[VE], b[VE];
+            params<T, LIE>(w, p.weight, p.w_f32, col(i), p.cols, 1.f);
+            params<T, LIE>(b, p.bias, p.w_f32, col(i), p.cols, 0.f);
+            h[i].get(f);
+#pragma unroll
+            for (int u = 0; u < VE; ++u) f[u] = (f[u] - mean) * rstd * w[u] + b[u];
+            put<T, LIE>(f, reinterpret_cast<char*>(static_cast<T*>(p.y) + base + col(i)), col(i), p.cols);
+        }
+}
+
 // Rows too long for a CTA's registers: three passes, re-reading the row (h,
 // where there is a residual) from the caches.
 template <typename T, int VE>
@@ -613,6 +706,120 @@ __global__ void __launch_bounds__(C, ctas_for(V * kVe<T, LIE>, C, GROUP))
     }
 }
 
+// Rows of more columns than the ring's threads hold: one CTA an SM walks over
+// rows gridDim.x apart (a multiple of 8 where there are several, so its threads
+// keep their columns off the grid too).  A row stays in registers in its own
+// type between the sums and dx, the next one is on its way to L2, and a
+// thread's column sums stay in its own slots of shared memory.
+template <typename T, int LIE, int V>
+__global__ void __launch_bounds__(1024, 1) norm_grad_wide_kernel(NormGradParams p) {
+    extern __shared__ float4 s_sums[];
+    __shared__ float2 s_part[2][32];
+    ptx::pdl_launch_dependents();  // the launch that adds the sums waits for this one's end itself
+    constexpr int VE = kFull<T>, Q = VE / 4;
+    const int n = blockDim.x, wl = threadIdx.x & 31, nw = n >> 5;
+    // slots k of dw and V * Q + k of db, for columns col(k / Q) + 4 (k % Q) on
+    float4* sum = s_sums + threadIdx.x;
+#pragma unroll
+    for (int k = 0; k < 2 * V * Q; ++k) sum[k * n] = make_float4(0.f, 0.f, 0.f, 0.f);
+    const float inv_n = 1.0f / static_cast<float>(p.cols);
+    const int first = static_cast<int>(threadIdx.x) * VE - before<T, LIE>(static_cast<int64_t>(blockIdx.x) * p.cols);
+    auto col = [&](int i) { return i * n * VE + first; };
+    const int64_t step = static_cast<int64_t>(gridDim.x) * p.cols;
+    int64_t base = static_cast<int64_t>(blockIdx.x) * p.cols;
+    int turn = 0;
+    for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, base += step, turn ^= 1) {
+        const T *h = static_cast<const T*>(p.h) + base, *dy = static_cast<const T*>(p.dy) + base;
+        const T* dh = static_cast<const T*>(p.dh) + base;
+        T* dx = static_cast<T*>(p.dx) + base;
+        const bool more = row + 1 < p.rows;
+        const float mean = p.mean[row], rstd = p.rstd[row];
+        Vec<T, VE> hv[V], gv[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            hv[i].w = gv[i].w = make_uint4(0, 0, 0, 0);
+            if (col(i) < p.cols) {
+                hv[i] = piece<T, LIE>(h + col(i), col(i), p.cols, more);
+                gv[i] = piece<T, LIE>(dy + col(i), col(i), p.cols, more);
+            }
+        }
+        if (row + gridDim.x < p.rows && threadIdx.x % 8 == 0) {
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (col(i) < p.cols) {
+                    ptx::prefetch_l2(h + step + col(i));
+                    ptx::prefetch_l2(dy + step + col(i));
+                    if (p.dh) ptx::prefetch_l2(dh + step + col(i));
+                }
+        }
+        float sa = 0.f, sx = 0.f, w[VE], f[VE], g[VE];
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (col(i) < p.cols) {
+                params<T, LIE>(w, p.weight, p.w_f32, col(i), p.cols, 1.f);
+                hv[i].get(f);
+                gv[i].get(g);
+#pragma unroll
+                for (int u = 0; u < VE; ++u) {
+                    const float a = g[u] * w[u];
+                    sa += a;
+                    sx += a * (f[u] - mean);
+                }
+            }
+        // two sets in turn: a set is written again only after the barrier of
+        // the row between
+        sa = lanes_sum(sa, 32);
+        sx = lanes_sum(sx, 32);
+        if (wl == 0) s_part[turn][threadIdx.x >> 5] = make_float2(sa, sx);
+        __syncthreads();
+        const float2 t = wl < nw ? s_part[turn][wl] : make_float2(0.f, 0.f);
+        const float ma = lanes_sum(t.x, 32) * inv_n, mx = lanes_sum(t.y, 32) * inv_n * rstd * rstd;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (col(i) < p.cols) {
+                float e[VE];
+                if (p.dh) piece<T, LIE>(dh + col(i), col(i), p.cols, more).get(e);
+                params<T, LIE>(w, p.weight, p.w_f32, col(i), p.cols, 1.f);
+                hv[i].get(f);
+                gv[i].get(g);
+                if (p.partial) {
+#pragma unroll
+                    for (int q = 0; q < Q; ++q) {
+                        float4 dw = sum[(i * Q + q) * n], db = sum[((V + i) * Q + q) * n];
+                        float *to = &dw.x, *tb = &db.x;
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) {
+                            to[u] += g[4 * q + u] * ((f[4 * q + u] - mean) * rstd);
+                            tb[u] += g[4 * q + u];
+                        }
+                        sum[(i * Q + q) * n] = dw;
+                        sum[((V + i) * Q + q) * n] = db;
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < VE; ++u)
+                    f[u] = rstd * (g[u] * w[u] - ma - (f[u] - mean) * mx) + (p.dh ? e[u] : 0.f);
+                put<T, LIE>(f, reinterpret_cast<char*>(dx + col(i)), col(i), p.cols);
+            }
+    }
+    if (!p.partial) return;
+    float* part = p.partial + static_cast<int64_t>(blockIdx.x) * 2 * p.cols;
+#pragma unroll
+    for (int k = 0; k < 2 * V * Q; ++k) {
+        const int c = col(k % (V * Q) / Q) + k % Q * 4;
+        const float4 t = sum[k * n];
+        float* to = part + (k < V * Q ? 0 : p.cols) + c;
+        if (LIE == kGrid) {
+            if (c < p.cols) *reinterpret_cast<float4*>(to) = t;
+        } else {
+            const float e[4] = {t.x, t.y, t.z, t.w};
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                if (c + u >= 0 && c + u < p.cols) to[u] = e[u];
+        }
+    }
+}
+
 // Long rows: dx alone, the row re-read from the caches.
 template <typename T, int VE>
 __global__ void __launch_bounds__(1024) norm_grad_long_kernel(NormGradParams p) {
@@ -777,6 +984,10 @@ cudaError_t launch_rows(K kernel, const P& p, int L, int ctas_per_sm, int max_ct
     return launch_kernel(kernel, dim3(static_cast<unsigned>(ctas)), dim3(threads), kSmem, st, false, p, L);
 }
 
+// Accesses that the threads of a kernel for wide rows hold, and threads.
+constexpr int kNormWide = 1024 * 4, kGradWide = 1024 * 4, kGradWideSmem = 224 << 10;
+int wide_threads(int nvec, int V) { return ((nvec + V - 1) / V + 31) & ~31; }
+
 // Elements of an access of the long rows' kernels.
 template <typename T, int LIE>
 constexpr int kLong = LIE == kGrid ? kFull<T> : 1;
@@ -810,9 +1021,15 @@ cudaError_t launch_norm_t(const NormParams& p, cudaStream_t st) {
     constexpr int VE = kVe<T, LIE>;
     return by_row<VE, VE == 1 ? 1 : 2, VE == 1 ? 4 : 1, 16>(accesses<T, LIE>(p.cols), [&](auto v, auto c, auto group, int L) {
         constexpr int V = v.value, C = c.value, S = 2;
-        if constexpr (V == 0)
+        if constexpr (V == 0) {
+            const int nvec = accesses<T, LIE>(p.cols);
+            if constexpr (LIE != kSingle) {
+                if (nvec <= kNormWide)
+                    return launch_kernel(norm_wide_kernel<T, LIE, 4>, dim3(static_cast<unsigned>(p.rows)),
+                                         dim3(wide_threads(nvec, 4)), 0, st, false, p);
+            }
             return launch_kernel(norm_long_kernel<T, kLong<T, LIE>>, dim3(static_cast<unsigned>(p.rows)), dim3(1024), 0, st, false, p);
-        else
+        } else
             return launch_rows<Ring<T, LIE, V, S, 2, C, group.value>, C, group.value>(norm_kernel<T, LIE, V, S, C, group.value>, p, L,
                                                                         ctas_for(V * VE, C, group.value), 1 << 30, nullptr, st);
     });
@@ -828,6 +1045,21 @@ cudaError_t launch_norm_grad_t(const NormGradParams& p, cudaStream_t st) {
         e = by_row<VE, VE == 1 ? 1 : 2, VE == 1 ? 4 : 2, 16>(accesses<T, LIE>(p.cols), [&](auto v, auto c, auto group, int L) {
             constexpr int V = v.value, C = c.value, S = stages_for(V * VE * sizeof(T));
             if constexpr (V == 0) {
+                const int nvec = accesses<T, LIE>(p.cols);
+                if constexpr (LIE != kSingle) {
+                    auto wide = [&](auto v) {
+                        const auto kernel = norm_grad_wide_kernel<T, LIE, v.value>;
+                        const int threads = wide_threads(nvec, v.value), smem = v.value * VE * threads * 8;
+                        const cudaError_t r =
+                            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kGradWideSmem);
+                        if (r != cudaSuccess) return r;
+                        parts = static_cast<int>(std::min<int64_t>(p.rows, kSms));
+                        return launch_kernel(kernel, dim3(parts), dim3(threads), smem, st, false, p);
+                    };
+                    if (nvec <= kGradWide / 2) return wide(std::integral_constant<int, 2>{});
+                    if (nvec <= kGradWide && wide_threads(nvec, 4) * 4 * VE * 8 <= kGradWideSmem)
+                        return wide(std::integral_constant<int, 4>{});
+                }
                 // the column sums first: dx may take dy's place
                 constexpr int VL = kLong<T, LIE>;
                 parts = static_cast<int>(p.rows < 64 ? p.rows : 64);

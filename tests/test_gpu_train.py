@@ -146,6 +146,32 @@ def test_layer_norm_many_rows_and_repeats(rows, cols, dtype):
         assert torch.equal(a, c)  # no atomics: the same bits
 
 
+# rows wider than the ring's threads hold, more of them than CTAs, on the grid
+# and off it, on either side of the kernels' limits (28672 columns of 16 bits and
+# 16384 of 32 in the gradient, 32768 and 16384 forward)
+@pytest.mark.parametrize("rows,cols,dtype", [
+    (1, 8200, BF), (333, 8200, BF), (309, 9001, BF), (160, 16384, HF), (157, 16392, BF), (155, 28672, BF),
+    (40, 28680, BF), (159, 20001, HF), (3, 32761, HF), (40, 32768, BF), (305, 8196, FP), (200, 8193, FP),
+    (155, 16384, FP), (40, 16388, FP), (5, 16381, FP)])
+def test_layer_norm_wide_rows(rows, cols, dtype):
+    g = gen(rows * 31 + cols)
+    x = randn(g, rows, cols, dtype=dtype, scale=2.0, shift=0.5)
+    w, b = randn(g, cols, scale=0.2, shift=1.0), randn(g, cols, scale=0.2)
+    res, dy, dh = (randn(g, rows, cols, dtype=dtype) for _ in range(3))
+    check_norm(x, w, b, None, 1e-5, *moe.moe_layer_norm(x, w, b))
+    y, h, mean, rstd = moe.moe_layer_norm(x, w, b, res)
+    check_norm(x, w, b, res, 1e-5, y, h, mean, rstd)
+    for dd, bias in ((None, True), (dh, True), (dh, False)):
+        got = moe.moe_layer_norm_backward(dy, h, mean, rstd, w, dh=dd, bias_grad=bias)
+        check_norm_grad(dy, h, mean, rstd, w, dd, *got)
+        for p, q in zip(got, moe.moe_layer_norm_backward(dy, h, mean, rstd, w, dh=dd, bias_grad=bias)):
+            assert p is q or torch.equal(p, q)
+    place = dy.clone()
+    for p, q in zip(moe.moe_layer_norm_backward(place, h, mean, rstd, w, dh=dh, dx=place),
+                    moe.moe_layer_norm_backward(dy, h, mean, rstd, w, dh=dh)):
+        assert torch.equal(p, q)
+
+
 def test_layer_norm_gradient_matches_differences():
     g = gen(3)
     rows, cols, eps = 3, 10, 1e-3
