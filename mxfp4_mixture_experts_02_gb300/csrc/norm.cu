@@ -152,6 +152,8 @@ __device__ __forceinline__ float half_of(float2 v, int second) { return second ?
 constexpr int kGroupThreads = 128;  // CTA of a kernel whose rows take a group of lanes
 constexpr int kNormCluster = 8;     // CTAs of the gradient for few rows
 constexpr int kRowThreads = 512;    // largest CTA of a kernel whose rows take the CTA
+constexpr int kNormWide = 4;        // accesses of a thread of norm_wide_kernel
+constexpr int kGradWideCols = 16;   // columns of a thread of norm_grad_wide_kernel
 
 // Resident CTAs of C threads by the columns of a thread: with up to eight, 64
 // registers a thread are enough, 80 for groups.
@@ -336,11 +338,13 @@ __device__ __forceinline__ Vec<T, kFull<T>> piece(const T* p, int c, int cols, b
 }
 
 // Rows of more columns than the ring's threads hold: a CTA per row, which stays
-// in registers in its own type; weights come from the caches.
-template <typename T, int LIE, int V>
+// in registers in its own type; weights come from the caches.  8138 x 12288 bf16
+// with a residual take 131 us (6.1 TB/s), three passes over the caches 263;
+// 8137 x 12289, whose weights are loaded one by one, 259.
+template <typename T, int LIE>
 __global__ void __launch_bounds__(1024, 1) norm_wide_kernel(NormParams p) {
     __shared__ float s_part[2][32];
-    constexpr int VE = kFull<T>;
+    constexpr int VE = kFull<T>, V = kNormWide;
     const int64_t base = static_cast<int64_t>(blockIdx.x) * p.cols;
     const bool more = blockIdx.x + 1 < p.rows;
     const int n = blockDim.x, first = static_cast<int>(threadIdx.x) * VE - before<T, LIE>(base);
@@ -403,7 +407,7 @@ __global__ void __launch_bounds__(1024, 1) norm_wide_kernel(NormParams p) {
         }
 }
 
-// Rows too long for a CTA's registers: three passes, re-reading the row (h,
+// Rows too long for a CTA's registers, or long and element by element: three passes, re-reading the row (h,
 // where there is a residual) from the caches.
 template <typename T, int VE>
 __global__ void __launch_bounds__(1024) norm_long_kernel(NormParams p) {
@@ -710,21 +714,42 @@ __global__ void __launch_bounds__(C, ctas_for(V * kVe<T, LIE>, C, GROUP))
 // rows gridDim.x apart (a multiple of 8 where there are several, so its threads
 // keep their columns off the grid too).  A row stays in registers in its own
 // type between the sums and dx, the next one is on its way to L2, and a
-// thread's column sums stay in its own slots of shared memory.
-template <typename T, int LIE, int V>
+// thread's weights and column sums stay in its own slots of shared memory.
+// Bound by the row's turn, in which loads, sums and stores follow one another:
+// 8138 x 12288 bf16 with dh take 171 us (4.7 TB/s), 237 without the prefetch,
+// 188 with the weights from the caches, 195 with dh loaded before the sums, 225
+// in two CTAs of half the threads an SM with the weights from the caches; dx
+// and column sums in two kernels 269.
+template <typename T, int LIE>
 __global__ void __launch_bounds__(1024, 1) norm_grad_wide_kernel(NormGradParams p) {
-    extern __shared__ float4 s_sums[];
+    extern __shared__ float4 s_cols[];
     __shared__ float2 s_part[2][32];
     ptx::pdl_launch_dependents();  // the launch that adds the sums waits for this one's end itself
-    constexpr int VE = kFull<T>, Q = VE / 4;
+    constexpr int VE = kFull<T>, Q = VE / 4, V = kGradWideCols / VE;
     const int n = blockDim.x, wl = threadIdx.x & 31, nw = n >> 5;
-    // slots k of dw and V * Q + k of db, for columns col(k / Q) + 4 (k % Q) on
-    float4* sum = s_sums + threadIdx.x;
+    // slots k of dw, V * Q + k of db and 2 * V * Q + k of the weights, for
+    // columns col(k / Q) + 4 (k % Q) on
+    float4 *sum = s_cols + threadIdx.x, *weight = sum + 2 * V * Q * n;
 #pragma unroll
     for (int k = 0; k < 2 * V * Q; ++k) sum[k * n] = make_float4(0.f, 0.f, 0.f, 0.f);
     const float inv_n = 1.0f / static_cast<float>(p.cols);
     const int first = static_cast<int>(threadIdx.x) * VE - before<T, LIE>(static_cast<int64_t>(blockIdx.x) * p.cols);
     auto col = [&](int i) { return i * n * VE + first; };
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        float w[VE];
+        params<T, LIE>(w, p.weight, p.w_f32, col(i), p.cols, 1.f);
+#pragma unroll
+        for (int q = 0; q < Q; ++q)
+            weight[(i * Q + q) * n] = make_float4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+    }
+    auto weights = [&](float (&w)[VE], int i) {
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+            const float4 t = weight[(i * Q + q) * n];
+            w[4 * q] = t.x, w[4 * q + 1] = t.y, w[4 * q + 2] = t.z, w[4 * q + 3] = t.w;
+        }
+    };
     const int64_t step = static_cast<int64_t>(gridDim.x) * p.cols;
     int64_t base = static_cast<int64_t>(blockIdx.x) * p.cols;
     int turn = 0;
@@ -756,7 +781,7 @@ __global__ void __launch_bounds__(1024, 1) norm_grad_wide_kernel(NormGradParams 
 #pragma unroll
         for (int i = 0; i < V; ++i)
             if (col(i) < p.cols) {
-                params<T, LIE>(w, p.weight, p.w_f32, col(i), p.cols, 1.f);
+                weights(w, i);
                 hv[i].get(f);
                 gv[i].get(g);
 #pragma unroll
@@ -779,7 +804,7 @@ __global__ void __launch_bounds__(1024, 1) norm_grad_wide_kernel(NormGradParams 
             if (col(i) < p.cols) {
                 float e[VE];
                 if (p.dh) piece<T, LIE>(dh + col(i), col(i), p.cols, more).get(e);
-                params<T, LIE>(w, p.weight, p.w_f32, col(i), p.cols, 1.f);
+                weights(w, i);
                 hv[i].get(f);
                 gv[i].get(g);
                 if (p.partial) {
@@ -820,7 +845,9 @@ __global__ void __launch_bounds__(1024, 1) norm_grad_wide_kernel(NormGradParams 
     }
 }
 
-// Long rows: dx alone, the row re-read from the caches.
+// Rows past 16384 columns, or long and element by element: dx alone, the row
+// re-read from the caches.  4882 x 20480 bf16 with dh take 239 us (3.3 TB/s) with
+// the column sums.
 template <typename T, int VE>
 __global__ void __launch_bounds__(1024) norm_grad_long_kernel(NormGradParams p) {
     __shared__ float s_part[2][32];
@@ -984,8 +1011,7 @@ cudaError_t launch_rows(K kernel, const P& p, int L, int ctas_per_sm, int max_ct
     return launch_kernel(kernel, dim3(static_cast<unsigned>(ctas)), dim3(threads), kSmem, st, false, p, L);
 }
 
-// Accesses that the threads of a kernel for wide rows hold, and threads.
-constexpr int kNormWide = 1024 * 4, kGradWide = 1024 * 4, kGradWideSmem = 224 << 10;
+// Threads for V accesses of each.
 int wide_threads(int nvec, int V) { return ((nvec + V - 1) / V + 31) & ~31; }
 
 // Elements of an access of the long rows' kernels.
@@ -1024,9 +1050,9 @@ cudaError_t launch_norm_t(const NormParams& p, cudaStream_t st) {
         if constexpr (V == 0) {
             const int nvec = accesses<T, LIE>(p.cols);
             if constexpr (LIE != kSingle) {
-                if (nvec <= kNormWide)
-                    return launch_kernel(norm_wide_kernel<T, LIE, 4>, dim3(static_cast<unsigned>(p.rows)),
-                                         dim3(wide_threads(nvec, 4)), 0, st, false, p);
+                if (nvec <= 1024 * kNormWide)
+                    return launch_kernel(norm_wide_kernel<T, LIE>, dim3(static_cast<unsigned>(p.rows)),
+                                         dim3(wide_threads(nvec, kNormWide)), 0, st, false, p);
             }
             return launch_kernel(norm_long_kernel<T, kLong<T, LIE>>, dim3(static_cast<unsigned>(p.rows)), dim3(1024), 0, st, false, p);
         } else
@@ -1047,18 +1073,17 @@ cudaError_t launch_norm_grad_t(const NormGradParams& p, cudaStream_t st) {
             if constexpr (V == 0) {
                 const int nvec = accesses<T, LIE>(p.cols);
                 if constexpr (LIE != kSingle) {
-                    auto wide = [&](auto v) {
-                        const auto kernel = norm_grad_wide_kernel<T, LIE, v.value>;
-                        const int threads = wide_threads(nvec, v.value), smem = v.value * VE * threads * 8;
+                    constexpr int VW = kGradWideCols / VE;
+                    if (nvec <= 1024 * VW) {
+                        const auto kernel = norm_grad_wide_kernel<T, LIE>;
+                        constexpr int kThread = kGradWideCols * 3 * sizeof(float);
+                        const int threads = wide_threads(nvec, VW);
                         const cudaError_t r =
-                            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kGradWideSmem);
+                            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 1024 * kThread);
                         if (r != cudaSuccess) return r;
                         parts = static_cast<int>(std::min<int64_t>(p.rows, kSms));
-                        return launch_kernel(kernel, dim3(parts), dim3(threads), smem, st, false, p);
-                    };
-                    if (nvec <= kGradWide / 2) return wide(std::integral_constant<int, 2>{});
-                    if (nvec <= kGradWide && wide_threads(nvec, 4) * 4 * VE * 8 <= kGradWideSmem)
-                        return wide(std::integral_constant<int, 4>{});
+                        return launch_kernel(kernel, dim3(parts), dim3(threads), threads * kThread, st, false, p);
+                    }
                 }
                 // the column sums first: dx may take dy's place
                 constexpr int VL = kLong<T, LIE>;

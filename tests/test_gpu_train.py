@@ -147,8 +147,8 @@ def test_layer_norm_many_rows_and_repeats(rows, cols, dtype):
 
 
 # rows wider than the ring's threads hold, more of them than CTAs, on the grid
-# and off it, on either side of the kernels' limits (28672 columns of 16 bits and
-# 16384 of 32 in the gradient, 32768 and 16384 forward)
+# and off it, on either side of the kernels' limits (16384 columns in the
+# gradient, 32768 of 16 bits and 16384 of 32 forward)
 @pytest.mark.parametrize("rows,cols,dtype", [
     (1, 8200, BF), (333, 8200, BF), (309, 9001, BF), (160, 16384, HF), (157, 16392, BF), (155, 28672, BF),
     (40, 28680, BF), (159, 20001, HF), (3, 32761, HF), (40, 32768, BF), (305, 8196, FP), (200, 8193, FP),
