@@ -530,8 +530,8 @@ typedef struct moe_adamw_tensor {
     int64_t n;
 } moe_adamw_tensor;
 
-/* step counts from 1; 0 <= beta < 1; eps >= 0; g_dtype MOE_DTYPE_BF16 or
- * MOE_DTYPE_F32; seed: of the MXFP8 states' rounding, another one each step. */
+/* step counts from 1; 0 <= beta < 1; eps >= 0; g_dtype: a MOE_DTYPE_*;
+ * seed: of the MXFP8 states' rounding, another one each step. */
 typedef struct moe_adamw_config {
     double lr, beta1, beta2, eps, weight_decay;
     int64_t step;

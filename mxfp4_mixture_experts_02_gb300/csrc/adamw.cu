@@ -166,7 +166,17 @@ __device__ __forceinline__ void load_some(float (&g)[kE], const G* p, int live) 
 
 // Eight gradients as they were read.
 template <typename G>
-struct Grad8;
+struct Grad8 {
+    static_assert(sizeof(G) == 2, "one access");
+    Vec<G, kE> v;
+    __device__ __forceinline__ void load(const G* p, bool) { v.w = ptx::ld_global_16(p); }
+    __device__ __forceinline__ void load_some(const G* p, int live) {
+        float f[kE];
+        moe::load_some(f, p, live);
+        v.set(f);
+    }
+    __device__ __forceinline__ void get(float (&g)[kE]) const { v.get(g); }
+};
 template <>
 struct Grad8<float> {
     float f[kE];
@@ -176,17 +186,6 @@ struct Grad8<float> {
 #pragma unroll
         for (int u = 0; u < kE; ++u) g[u] = f[u];
     }
-};
-template <>
-struct Grad8<__nv_bfloat16> {
-    Vec<__nv_bfloat16, 8> v;
-    __device__ __forceinline__ void load(const __nv_bfloat16* p, bool) { v.w = ptx::ld_global_16(p); }
-    __device__ __forceinline__ void load_some(const __nv_bfloat16* p, int live) {
-        float f[kE];
-        moe::load_some(f, p, live);
-        v.set(f);
-    }
-    __device__ __forceinline__ void get(float (&g)[kE]) const { v.get(g); }
 };
 
 __device__ __forceinline__ void store8(float* p, const float (&v)[kE], bool by32) {
@@ -413,8 +412,13 @@ cudaError_t launch_adamw(const AdamwBatch<N>& b, int g_dtype, bool mx, cudaStrea
     const uint32_t most = kSms * (mx ? kAdamwCtas<true> : kAdamwCtas<false>);
     const dim3 grid(b.items < most ? b.items : most);
     auto go = [&](auto kernel) { return launch_kernel(kernel, grid, dim3(kAdamwThreads), 0, st, false, b); };
-    if (g_dtype == MOE_DTYPE_F32) return mx ? go(adamw_kernel<float, true, N>) : go(adamw_kernel<float, false, N>);
-    return mx ? go(adamw_kernel<__nv_bfloat16, true, N>) : go(adamw_kernel<__nv_bfloat16, false, N>);
+    auto by_grad = [&](auto g) {
+        using G = decltype(g);
+        return mx ? go(adamw_kernel<G, true, N>) : go(adamw_kernel<G, false, N>);
+    };
+    return g_dtype == MOE_DTYPE_F32   ? by_grad(float{})
+           : g_dtype == MOE_DTYPE_F16 ? by_grad(__half{})
+                                      : by_grad(__nv_bfloat16{});
 }
 
 template cudaError_t launch_adamw<kAdamwFew>(const AdamwBatch<kAdamwFew>&, int, bool, cudaStream_t);

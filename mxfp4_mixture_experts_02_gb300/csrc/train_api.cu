@@ -128,7 +128,7 @@ int step_some(const moe_adamw_tensor* tensors, int32_t count, int32_t& i, const 
         if (items + mine > 0xFFFFFFFFll) break;
         AdamwTensor& k = b->t[b->count++];
         k = AdamwTensor{t.p, t.g, t.m, t.v, t.m_scale, t.v_scale, t.n, counter, static_cast<uint32_t>(items), 0};
-        const auto wide = [&](uintptr_t a) {  // bf16 gradients take 16 bytes, codes 8
+        const auto wide = [&](uintptr_t a) {  // 16-bit gradients take 16 bytes, codes 8
             return on(t.p, a) && on(t.g, c.g_dtype == MOE_DTYPE_F32 ? a : 16) && (mx ? all_on(8, t.m, t.v) : all_on(a, t.m, t.v));
         };
         k.vec = wide(32) ? 2 : wide(16) ? 1 : 0;
@@ -296,7 +296,7 @@ int moe_route_backward(const moe_token_shape* s, const uint16_t* shared_logit, f
 int moe_adamw(const moe_adamw_tensor* tensors, int32_t count, const moe_adamw_config* c, const float* grad_scale,
               moe_stream_t stream) {
     if (!c || (count > 0 && !tensors)) return MOE_ERR_NULL;
-    if (count < 0 || c->step < 1 || (c->g_dtype != MOE_DTYPE_BF16 && c->g_dtype != MOE_DTYPE_F32)) return MOE_ERR_SHAPE;
+    if (count < 0 || c->step < 1 || c->g_dtype < MOE_DTYPE_BF16 || c->g_dtype > MOE_DTYPE_F32) return MOE_ERR_SHAPE;
     if (c->state != MOE_STATE_F32 && c->state != MOE_STATE_MXFP8) return MOE_ERR_SHAPE;
     auto in01 = [](double v) { return v >= 0.0 && v < 1.0; };
     auto finite = [](double v) { return v >= -3.0e38 && v <= 3.0e38; };

@@ -365,8 +365,8 @@ def moe_route_backward(shape: MoeTokenShape, topk_ids, topk_w, dtopk_w, shared_l
 
 # ------------------------------------------------------------------ AdamW
 class MoeAdamwTensors:
-    """The tensors of moe_adamw, checked once: lists of params (fp32), grads (bf16
-    or fp32) and states, entry i of each belonging together.  States are fp32 m and
+    """The tensors of moe_adamw, checked once: lists of params (fp32), grads (bf16,
+    fp16 or fp32) and states, entry i of each belonging together.  States are fp32 m and
     v, or uint8 E4M3 codes of m and sqrt(v) with uint8 E8M0 scales (one per 32
     elements).  The object holds the tensors; gradients are read from these
     buffers at every step (accumulate into them, or build another object)."""
@@ -382,8 +382,8 @@ class MoeAdamwTensors:
         self.state = STATE_MXFP8 if mx else STATE_F32
         self.index = _index("params[0]", params[0]) if params else 0
         g_dtype = grads[0].dtype if grads else torch.float32
-        if g_dtype not in (torch.bfloat16, torch.float32):
-            raise ValueError("grads: expected bfloat16 or float32, got %s" % g_dtype)
+        if g_dtype not in _DTYPES:
+            raise ValueError("grads: expected bfloat16, float16 or float32, got %s" % g_dtype)
         self.g_dtype = _DTYPES[g_dtype]
         s_dtype = torch.uint8 if mx else torch.float32
         for i, p in enumerate(params):

@@ -516,7 +516,7 @@ def adamw_ref(p, g, m, v, step, scale, lr, betas, eps, weight_decay):
 SIZES = [1, 7, 31, 32, 33, 4095, 4096, 4097, 100003, 0, 512 * 128]
 
 
-@pytest.mark.parametrize("g_dtype", [FP, BF])
+@pytest.mark.parametrize("g_dtype", [FP, BF, HF])
 @pytest.mark.parametrize("scale", [None, 0.37])
 def test_adamw_f32(g_dtype, scale):
     g = gen(1)
@@ -590,7 +590,7 @@ def check_mx(codes, scales, value, err, rand16, root):
     assert ((got == 0) | (torch.sign(got) == torch.sign(value))).all()
 
 
-@pytest.mark.parametrize("g_dtype", [FP, BF])
+@pytest.mark.parametrize("g_dtype", [FP, BF, HF])
 def test_adamw_mxfp8(g_dtype):
     sizes = [1, 7, 31, 32, 33, 4097, 0, 20000]
     g = gen(2)

@@ -137,7 +137,7 @@ def test_adamw_arguments_refused():
     assert L.moe_adamw(ok, 1, None, None, None) == NULL
     assert L.moe_adamw(None, 1, adamw_config(), None, None) == NULL
     assert L.moe_adamw(None, 0, adamw_config(), None, None) == 0
-    for kw in (dict(step=0), dict(g_dtype=1), dict(state=2), dict(beta1=1.0), dict(beta1=-0.1), dict(beta2=1.0),
+    for kw in (dict(step=0), dict(g_dtype=3), dict(g_dtype=-1), dict(state=2), dict(beta1=1.0), dict(beta1=-0.1), dict(beta2=1.0),
                dict(beta2=float("nan")), dict(lr=float("inf")), dict(eps=-1.0), dict(eps=float("nan")),
                dict(weight_decay=float("nan"))):
         assert L.moe_adamw(ok, 1, adamw_config(**kw), None, None) == SHAPE, kw
