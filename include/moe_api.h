@@ -485,8 +485,9 @@ int moe_token_map_workspace_bytes(const moe_token_shape* shape, size_t* bytes);
 int moe_token_map(const moe_token_shape* shape, const int32_t* topk_ids, int32_t* a_map, int32_t* c_map,
                   int32_t* expert_offsets, void* workspace, size_t workspace_bytes, moe_stream_t stream);
 
-/* rows[c_map[t, j]] = x[t]: x [T, H] -> rows [R, H] (rows from R on are not
- * touched).  Every c_map entry is -1 or a row of its own in `rows`. */
+/* rows[c_map[t, j]] = x[t]: x [T, H] -> the first R of rows [T * k', H] (rows
+ * from R on are not touched).  Here and below expert rows are a buffer of T * k'
+ * rows, and every c_map entry is -1 or a row of its own in it. */
 int moe_permute(const moe_token_shape* shape, const void* x, const int32_t* c_map, void* rows, moe_stream_t stream);
 
 /* dx[t] = sum over j with c_map[t, j] >= 0 of drows[c_map[t, j]], j ascending. */
