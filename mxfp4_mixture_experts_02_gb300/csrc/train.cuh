@@ -269,6 +269,7 @@ struct AdamwBatch {
 static_assert(sizeof(AdamwBatch<kAdamwMany>) <= 32764, "kernel parameters");
 
 constexpr int kAdamwStep = 2048;  // elements that a CTA takes at once: eight for each thread
+constexpr int kAdamwItem = 8;     // most steps of a work item
 
 template <int N>
 cudaError_t launch_adamw(const AdamwBatch<N>& b, int g_dtype, bool mx, cudaStream_t st);

@@ -119,7 +119,7 @@ int step_some(const moe_adamw_tensor* tensors, int32_t count, int32_t& i, const 
     // items of up to eight steps, eight items for each of four CTAs on an SM
     int64_t total = 0;
     for (int32_t j = i, taken = 0; j < count && taken < N; ++j) taken += tensors[j].n > 0, total += tensors[j].n;
-    b->item_elems = kAdamwStep * static_cast<int>(std::clamp<int64_t>(total / (int64_t(kAdamwStep) * kSms * 32), 1, 8));
+    b->item_elems = kAdamwStep * static_cast<int>(std::clamp<int64_t>(total / (int64_t(kAdamwStep) * kSms * 32), 1, kAdamwItem));
     int64_t items = 0;
     for (; i < count && b->count < N; ++i) {
         const moe_adamw_tensor& t = tensors[i];
