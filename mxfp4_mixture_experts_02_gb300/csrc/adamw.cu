@@ -6,10 +6,10 @@
 // the states follow from them alone.
 //
 // With fp32 states the bytes bind: 128 M parameters and bf16 gradients (26
-// bytes each) take 504 us, 6.6 TB/s.  With MXFP8 states (14.1 bytes) the update
-// binds, about 60 instructions an element of which the 64-bit random numbers
-// are 10 and the two codes 14: 96 M take 256 us, 5.3 TB/s, and fp32 gradients
-// hardly more.
+// bytes each) take 504 us, 6.6 TB/s.  With MXFP8 states (14.1 bytes) 96 M take
+// 229 us, 5.9 TB/s: reads wait behind the update's 60 instructions an element
+// (of which the 64-bit random numbers are 10 and the two codes 14); with fp32
+// gradients (18.1 bytes) 244 us, 6.3 TB/s.
 //
 // 8-bit states: m and sqrt(v) as E4M3 codes with one power-of-two scale per
 // 32 values, 2^e with e = floor(log2 max) - 7 (the largest magnitude lies in
@@ -30,7 +30,8 @@ constexpr int kE = 8;  // elements per thread: four threads share a block of 32
 // Resident CTAs.  With fp32 states two keep memory busy (128 M parameters: 505
 // us, 522 with four); with MXFP8 states the update has about as many
 // instructions as its bytes allow time for, and four hide its latencies better
-// than registers that would hold the next step (96 M: 257 us, 262 with three).
+// than registers that would hold the next step (96 M: 229 us; 238 with three,
+// 248 with five; with the next step in registers 247, three 256).
 template <bool MX>
 constexpr uint32_t kAdamwCtas = MX ? 4 : 2;
 constexpr uint64_t kGamma = 0x9E3779B97F4A7C15ull;
@@ -270,11 +271,15 @@ __device__ __forceinline__ void fetch(Step<G, MX>& s, const ItemPtrs<G>& t, uint
     }
 }
 
-// A step's lines into L2, by the threads whose elements begin them.
+// A step's lines into L2, by the threads whose elements begin them: all with
+// 16-bit gradients (96 M elements with MXFP8 states 229 us, codes alone 232,
+// none 235), the codes' with fp32 gradients (244 us, all 290, none 243).
 template <typename G>
 __device__ __forceinline__ void prefetch(const ItemPtrs<G>& t, uint32_t o) {
-    if (threadIdx.x % 4 == 0) ptx::prefetch_l2(t.p + o);
-    if (threadIdx.x % (16 / sizeof(G)) == 0) ptx::prefetch_l2(t.g + o);
+    if constexpr (sizeof(G) == 2) {
+        if (threadIdx.x % 4 == 0) ptx::prefetch_l2(t.p + o);
+        if (threadIdx.x % 8 == 0) ptx::prefetch_l2(t.g + o);
+    }
     if (threadIdx.x % 16 == 0) {
         ptx::prefetch_l2(static_cast<const uint8_t*>(t.m) + o);
         ptx::prefetch_l2(static_cast<const uint8_t*>(t.v) + o);
