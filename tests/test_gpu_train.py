@@ -658,6 +658,65 @@ def test_adamw_more_tensors_than_a_launch_takes_and_misaligned():
         within(flat[0], want, 4 * EPS * before.double().abs() + 40 * EPS * upd.abs())
 
 
+@pytest.mark.parametrize("g_dtype", [BF, FP])
+def test_adamw_mxfp8_long_tensors_and_scales_anywhere(g_dtype):
+    """Work items of eight steps, the last of a tensor shorter, and scales off the 4-byte grid."""
+    g = gen(7)
+    sizes = [8 * 2048 * 152 * 32 + 5 * 2048 + 77, 3 * 2048 + 40, 70001]
+    ps = [randn(g, n, scale=0.1) for n in sizes]
+    gs = [(randn(g, n) * torch.exp(3 * randn(g, n) - 6)).to(g_dtype) for n in sizes]
+    h = moe.adamw_tensors([p.clone() for p in ps], gs, mxfp8=True)
+    blocks = [(n + 31) // 32 for n in sizes]
+    flat = torch.zeros(sum(blocks) * 2 + 3, dtype=torch.uint8, device="cuda")
+    cuts = torch.split(flat[3:], blocks * 2)
+    odd = moe.MoeAdamwTensors([p.clone() for p in ps], gs, [torch.zeros_like(m) for m in h.m],
+                              [torch.zeros_like(v) for v in h.v], list(cuts[:3]), list(cuts[3:]))
+    for step in (1, 2):
+        old = [(p.clone(), mx_decode(m, ms), mx_decode(v, vs)) for p, m, ms, v, vs in
+               zip(h.params[1:], h.m[1:], h.m_scale[1:], h.v[1:], h.v_scale[1:])]
+        some = [0, 2048 * 8 - 64, 2048 * 8 * 1000 + 32 * 301, sizes[0] // 32 * 32 - 4096]
+        old += [(h.params[0][c:c + 4096].clone(), mx_decode(h.m[0][c:c + 4096], h.m_scale[0][c // 32:c // 32 + 128]),
+                 mx_decode(h.v[0][c:c + 4096], h.v_scale[0][c // 32:c // 32 + 128])) for c in some]
+        for t in (h, odd):
+            moe.moe_adamw(t, step, seed=step, **HYPER)
+        for name in ("params", "m", "v", "m_scale", "v_scale"):
+            assert all(torch.equal(p, q) for p, q in zip(getattr(h, name), getattr(odd, name))), name
+        first = (sizes[0] + 31) // 32 * 32
+        second = first + (sizes[1] + 31) // 32 * 32
+        at = [(1, 0, sizes[1], first), (2, 0, sizes[2], second)] + [(0, c, c + 4096, c) for c in some]
+        for (p0, m0, r0), (i, lo, hi, counter) in zip(old, at):
+            gr, b = gs[i][lo:hi], slice(lo // 32, (hi + 31) // 32)
+            want, wm, wv, upd = adamw_ref(p0, gr, m0, r0 * r0, step, 1.0, **HYPER)
+            gd = gr.double().abs()
+            mb, vb = 6 * EPS * (m0.abs() + gd), 8 * EPS * (r0 * r0 + gd * gd)
+            den = (wv / (1 - 0.999 ** step)).sqrt() + 1e-8
+            rel = 0.5 * vb / wv.clamp_min(1e-300) + 8 * EPS
+            within(h.params[i][lo:hi], want, 4 * EPS * p0.double().abs() + upd.abs() * rel
+                   + 2 * HYPER["lr"] * mb / den + 1e-30)
+            bits = random_halves(step, counter, hi - lo)
+            check_mx(h.m[i][lo:hi], h.m_scale[i][b], wm, mb, bits & 0xFFFF, False)
+            check_mx(h.v[i][lo:hi], h.v_scale[i][b], wv.sqrt(), wv.sqrt() * rel, bits >> 16, True)
+
+
+def test_adamw_mxfp8_non_finite_in_whole_steps():
+    n, at = 3 * 2048, (0, 2047, 2048 + 777)
+    p, gr = torch.ones(n, device="cuda"), randn(gen(8), n)
+    clean = moe.adamw_tensors([p.clone()], [gr.clone()], mxfp8=True)
+    gr[list(at)] = torch.tensor([float("nan"), float("inf"), float("-inf")], device="cuda")
+    h = moe.adamw_tensors([p], [gr], mxfp8=True)
+    for t in (clean, h):
+        moe.moe_adamw(t, 1, seed=3, **HYPER)
+    bad = torch.zeros(n, dtype=torch.bool, device="cuda")
+    bad[list(at)] = True
+    for t, s in (("m", "m_scale"), ("v", "v_scale")):
+        got = mx_decode(getattr(h, t)[0], getattr(h, s)[0])
+        assert torch.equal(torch.isnan(got), bad)
+        touched = bad.view(-1, 32).any(1)
+        assert torch.equal(getattr(h, s)[0][~touched], getattr(clean, s)[0][~touched])
+        assert torch.equal(getattr(h, t)[0].view(-1, 32)[~touched], getattr(clean, t)[0].view(-1, 32)[~touched])
+    assert torch.equal(h.params[0][~bad], clean.params[0][~bad]) and torch.isnan(h.params[0][bad]).all()
+
+
 @pytest.mark.parametrize("mx", [False, True])
 def test_adamw_skips_a_step_whose_scale_is_not_finite(mx):
     for bad in (float("inf"), float("nan")):
